@@ -32,7 +32,8 @@ EXPORTED = ("dgen_create", "dgen_destroy", "dgen_prefill_prompt", "dgen_set_prom
             "dgen_capture_routing", "dgen_debug_read", "dgen_sample_from_logits_noalloc",
             "dgen_set_flags", "dgen_expert_usage", "dgen_force_routing", "dgen_set_tuning",
             "dgen_generate_block_eb", "dgen_append_canvas", "dgen_generate", "dgen_capture_residual",
-            "dgen_gemm_e4m3", "dgen_set_self_cond", "dgen_gemm_bf16_pair")
+            "dgen_gemm_e4m3", "dgen_set_self_cond", "dgen_gemm_bf16_pair", "dgen_paged_append",
+            "dgen_paged_attention", "dgen_paged_workspace_bytes")
 PROBE_EXPORTED = ("dgen_gemm_rowsum_variant",)
 
 K_QKV, K_ATTENTION, K_OPROJ, K_ROUTER, K_EXPERT_GATE_UP, K_EXPERT_DOWN, K_SHARED_FFN, K_LM_HEAD, K_SAMPLER, \
@@ -59,6 +60,17 @@ class Weights(ctypes.Structure):
     _fields_ = [("embed", ctypes.c_void_p), ("final_norm", ctypes.c_void_p),
                 ("layers", ctypes.POINTER(LayerWeights)),
                 ("sc_norm", ctypes.c_void_p), ("w_sc_gate_up", ctypes.c_void_p), ("w_sc_down", ctypes.c_void_p)]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k_dev", "v_dev", "k_scale_dev", "v_scale_dev", "page_table_dev", "kv_len_dev")] + \
+        [(n, ctypes.c_int32) for n in (
+            "type", "n_pages", "n_kv_heads", "page_size", "head_dim", "batch", "table_pages", "table_stride")]
+
+
+class TokenRows(ctypes.Structure):
+    _fields_ = [("dev", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 _P, _I32, _I64, _U64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
@@ -97,6 +109,9 @@ _SIGS = {
     "dgen_debug_read": [_P, _I32, _I32, _P, _U64],
     "dgen_sample_from_logits_noalloc": [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _U64, _F, _F, _I32, _P, _P],
     "dgen_get_timing": [_P, _I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_I64)],
+    "dgen_paged_append": [_P, _I32, _P, _I32, _P, _P, _I32, _P, _P, _F, _P],
+    "dgen_paged_attention": [_P, _I32, _P, _I32, _I32, _P, _P, _F, _I32, _I32, _F, _P, _P, _I64, _P],
+    "dgen_paged_workspace_bytes": [],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -104,11 +119,12 @@ for _name, _args in _SIGS.items():
     _f.restype = ctypes.c_int
 _lib.dgen_status_str.restype = ctypes.c_char_p
 _lib.dgen_launch_count.restype = ctypes.c_int64
+_lib.dgen_paged_workspace_bytes.restype = ctypes.c_int64
 
 
 class DgenError(RuntimeError):
-    def __init__(self, call: str, status: int):
-        super().__init__(f"{call}: {status} ({_lib.dgen_status_str(status).decode()})")
+    def __init__(self, call: str, status: int, what: str = ""):
+        super().__init__(f"{call}: {status} ({_lib.dgen_status_str(status).decode()})" + (f": {what}" if what else ""))
         self.status = status
 
 
@@ -368,3 +384,6 @@ class Denoiser:
         ms, n = ctypes.c_double(), _I64()
         _check("dgen_get_timing", _lib.dgen_get_timing(self._h, cls, ctypes.byref(ms), ctypes.byref(n)))
         return ms.value, n.value
+
+
+from .paged import PagedCache, paged_append, paged_attention, paged_workspace  # noqa: E402,F401

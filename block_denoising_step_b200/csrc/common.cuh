@@ -132,7 +132,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t addr, uint32_t parity) {
     return ok != 0;
 }
 
-__device__ __noinline__ bool mbar_wait_slow(uint32_t addr, uint32_t parity, int* err, int code) {
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t addr, uint32_t parity, int* err, int code) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(addr, parity)) return true;

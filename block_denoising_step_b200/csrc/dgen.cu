@@ -38,29 +38,13 @@
 #include "gemm_pair.cuh"
 #include "gemm_tc.cuh"
 #include "kernels.cuh"
+#include "launch.cuh"
 
 using namespace dgen;
 
 namespace {
 
 // ------------------------------------------------------------------ tensor maps
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool load_encode() {
-    std::call_once(g_encode_once, [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-    });
-    return g_encode != nullptr;
-}
 
 // 2-D bf16 tensor [rows][cols] (row-major), box = 64 columns x box_rows rows,
 // 128-byte swizzle, zero fill outside the tensor.
@@ -97,46 +81,6 @@ bool make_map_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
 template <int BN>
 constexpr int stages_for() {
     return BN <= 64 ? 8 : (BN == 128 ? 6 : 4);
-}
-
-
-// Raise a kernel's dynamic shared-memory limit to at least `bytes` on a
-// device (kept per (kernel, device) and only ever raised: a kernel whose
-// dynamic size depends on the shape must not be capped by an earlier, smaller
-// launch).  Keyed on the kernel's address: instantiations that differ only in
-// tile size share a function type.
-std::mutex g_attr_mu;
-std::map<std::pair<const void*, int>, int> g_attr_bytes;
-
-template <class K>
-void set_smem_attr_once(K kern, int bytes, int dev) {
-    const void* f = reinterpret_cast<const void*>(kern);
-    std::lock_guard<std::mutex> lock(g_attr_mu);
-    int& cur = g_attr_bytes[{f, dev}];
-    if (bytes > cur) {
-        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        cur = bytes;
-    }
-}
-
-// Launch with the programmatic-stream-serialization attribute: the kernel may be
-// scheduled while its predecessor drains; each kernel waits (griddepcontrol)
-// before touching memory the predecessor writes.
-std::atomic<bool> g_pdl{true};  // cleared by DGEN_FLAG_NO_PDL on any handle (process-wide)
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_ex(cudaStream_t st, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, Args... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = g_pdl.load(std::memory_order_relaxed) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // KIND 0: bf16 operands; 1: E4M3 operands (K counted in elements either way).

@@ -1,0 +1,254 @@
+// Host side of the paged KV cache's C entry points (include/dgen.h): argument
+// checks, the choice of kernel, launches.  No handle: the calls launch on the
+// current device and keep nothing but per-device constants.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "dgen.h"
+#include "launch.cuh"
+#include "paged_append.cuh"
+#include "paged_split.cuh"
+
+using namespace dgen;
+
+namespace {
+
+constexpr int kMaxGrid = 1024;           // CTAs of an attention launch at most (its counters)
+constexpr size_t kCounterBytes = kMaxGrid * sizeof(unsigned int);
+constexpr int kMaxDevices = 64;
+
+int sm_count(int dev) {
+    static std::atomic<int> known[kMaxDevices];
+    if (dev < 0 || dev >= kMaxDevices) return 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// 16-byte access to every row: base and strides
+bool good_rows(const dgen_token_rows* r) {
+    return r && aligned16(r->dev) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+
+paged::RowsView view(const dgen_token_rows* r) {
+    return {static_cast<uint8_t*>(r->dev), r->token_stride, r->head_stride};
+}
+
+int check_cache(const dgen_paged_cache* c, int n_tokens, const int32_t* cu) {
+    if (!c || !aligned16(c->k_dev) || !aligned16(c->v_dev) || !c->page_table_dev || !c->kv_len_dev) return DGEN_EINVAL;
+    if (c->type != DGEN_TYPE_BF16 && c->type != DGEN_TYPE_F16 && c->type != DGEN_TYPE_E4M3) return DGEN_EINVAL;
+    if ((c->type == DGEN_TYPE_E4M3) != (c->k_scale_dev != nullptr) || !c->k_scale_dev != !c->v_scale_dev)
+        return DGEN_EINVAL;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DGEN_EINVAL;
+    if (c->n_pages < 1 || c->n_kv_heads < 1 || c->page_size < 1 || c->batch < 1 || c->table_pages < 1 ||
+        c->table_stride < c->table_pages)
+        return DGEN_EINVAL;
+    const int64_t rows = static_cast<int64_t>(c->n_pages) * c->n_kv_heads;  // rows of the cache count in 32 bits
+    if (rows > INT32_MAX || rows * c->page_size >= static_cast<int64_t>(UINT32_MAX)) return DGEN_EINVAL;
+    if (static_cast<int64_t>(c->table_pages) * c->page_size > (int64_t{1} << 30)) return DGEN_EINVAL;
+    if (n_tokens < 0 || (!cu && n_tokens % c->batch)) return DGEN_EINVAL;
+    return DGEN_OK;
+}
+
+paged::CacheView view(const dgen_paged_cache* c, int n_tokens, const int32_t* cu) {
+    paged::CacheView v{};
+    v.k = static_cast<uint8_t*>(c->k_dev);
+    v.v = static_cast<uint8_t*>(c->v_dev);
+    v.k_scale = c->k_scale_dev;
+    v.v_scale = c->v_scale_dev;
+    v.table = c->page_table_dev;
+    v.kv_len = c->kv_len_dev;
+    v.cu = cu;
+    v.n_pages = c->n_pages;
+    v.Hkv = c->n_kv_heads;
+    v.page = c->page_size;
+    v.B = c->batch;
+    v.table_stride = c->table_stride;
+    v.table_pages = c->table_pages;
+    v.n_tokens = n_tokens;
+    v.n_uniform = n_tokens / c->batch;
+    return v;
+}
+
+template <int HD, bool BF, bool E4M3>
+int launch_append(cudaStream_t st, const paged::AppendArgs& a, int per_block) {
+    const int blocks = (a.c.n_tokens + per_block - 1) / per_block;
+    return launch_ex(st, paged::paged_append_kernel<HD, BF, E4M3>, dim3(blocks), dim3(paged::kAppendThreads), 0, a,
+                     per_block) == cudaSuccess
+               ? DGEN_OK
+               : DGEN_ECUDA;
+}
+
+template <int HD>
+int append_hd(cudaStream_t st, const paged::AppendArgs& a, int per_block, bool bf, bool e4m3) {
+    if (bf) return e4m3 ? launch_append<HD, true, true>(st, a, per_block) : launch_append<HD, true, false>(st, a, per_block);
+    return e4m3 ? launch_append<HD, false, true>(st, a, per_block) : launch_append<HD, false, false>(st, a, per_block);
+}
+
+struct Workspace {
+    unsigned int* counters;
+    float* parts;
+    size_t floats;
+};
+
+template <int HD, int ES, bool BF, int NT>
+int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const Workspace& ws) {
+    using S = paged::SplitSmem<HD, ES, NT>;
+    a.p.R = S::R;
+    a.p.KB = paged::kBlockKeys;
+    const int per_sm = S::BYTES <= 112 * 1024 ? 2 : 1;
+    int64_t grid = std::min(kMaxGrid, sms * per_sm);
+    // no more CTAs than blocks of the longest possible line
+    const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
+    const int64_t tiles = std::min<int64_t>(rows, rows / S::R + a.c.B) * a.c.Hkv;
+    const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + paged::kBlockKeys - 1) / paged::kBlockKeys;
+    if (tiles < grid && tiles * blocks < grid) grid = std::max<int64_t>(1, tiles * blocks);
+    if (2 * static_cast<size_t>(grid) * S::R * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
+    auto kern = paged::paged_split_kernel<HD, ES, BF, NT>;
+    set_smem_attr_once(kern, S::BYTES, dev);
+    a.counters = ws.counters;
+    a.parts = ws.parts;
+    return launch_ex(st, kern, dim3(static_cast<unsigned>(grid)), dim3(paged::kSplitWarps * 32), S::BYTES, a) == cudaSuccess
+               ? DGEN_OK
+               : DGEN_ECUDA;
+}
+
+// Row tiles of 8, 16 or (hd <= 128: the accumulators of 32 rows of 256 would not
+// fit the registers) 32 query rows, by the rows a sequence has on average.
+template <int HD, int ES, bool BF>
+int split_rows(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, const Workspace& ws) {
+    const int64_t rows = (static_cast<int64_t>(a.c.n_tokens) + a.c.B - 1) / a.c.B * a.p.G;
+    if (rows <= 8) return launch_split<HD, ES, BF, 1>(st, dev, sms, a, ws);
+    if constexpr (HD <= 128)
+        if (rows > 16) return launch_split<HD, ES, BF, 4>(st, dev, sms, a, ws);
+    return launch_split<HD, ES, BF, 2>(st, dev, sms, a, ws);
+}
+
+template <int HD>
+int split_hd(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, const Workspace& ws, int cache_type) {
+    if (cache_type == DGEN_TYPE_E4M3) return split_rows<HD, 1, false>(st, dev, sms, a, ws);
+    if (cache_type == DGEN_TYPE_BF16) return split_rows<HD, 2, true>(st, dev, sms, a, ws);
+    return split_rows<HD, 2, false>(st, dev, sms, a, ws);
+}
+
+int append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, int32_t type, const dgen_token_rows* k,
+           const dgen_token_rows* v, int32_t n_q_heads, const dgen_token_rows* q, const dgen_token_rows* q_out,
+           float rope_base, void* stream) {
+    const int rc = check_cache(cache, n_tokens, cu);
+    if (rc != DGEN_OK) return rc;
+    if (type != DGEN_TYPE_BF16 && type != DGEN_TYPE_F16) return DGEN_EINVAL;
+    if (cache->type != DGEN_TYPE_E4M3 && cache->type != type) return DGEN_EINVAL;
+    if (n_q_heads < 0 || n_q_heads > 65536 || !(rope_base >= 0.f) || std::isinf(rope_base)) return DGEN_EINVAL;
+    if (n_tokens == 0) return DGEN_OK;
+    if (!good_rows(k) || !good_rows(v)) return DGEN_EINVAL;
+    if ((n_q_heads > 0) != (q != nullptr) || !q != !q_out) return DGEN_EINVAL;
+    if (q && (!good_rows(q) || !good_rows(q_out))) return DGEN_EINVAL;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DGEN_ECUDA;
+    const int sms = sm_count(dev);
+    if (sms < 1) return DGEN_ECUDA;
+    paged::AppendArgs a{};
+    a.c = view(cache, n_tokens, cu);
+    a.k = view(k);
+    a.v = view(v);
+    a.Hq = n_q_heads;
+    if (q) {
+        a.q = view(q);
+        a.q_out = view(q_out);
+    }
+    a.rotate = rope_base > 0.f;
+    a.log2_base = a.rotate ? std::log2(static_cast<double>(rope_base)) : 0.0;
+    const int per_block = std::clamp(n_tokens / (2 * sms), 1, paged::kAppendTokens);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool bf = type == DGEN_TYPE_BF16, e4 = cache->type == DGEN_TYPE_E4M3;
+    if (cache->head_dim == 64) return append_hd<64>(st, a, per_block, bf, e4);
+    if (cache->head_dim == 128) return append_hd<128>(st, a, per_block, bf, e4);
+    return append_hd<256>(st, a, per_block, bf, e4);
+}
+
+int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, int32_t type, int32_t n_q_heads,
+           const dgen_token_rows* q, const dgen_token_rows* out, float scale, int32_t causal, int32_t window, float cap,
+           float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+    const int rc = check_cache(cache, n_tokens, cu);
+    if (rc != DGEN_OK) return rc;
+    if (type != DGEN_TYPE_BF16 && type != DGEN_TYPE_F16) return DGEN_EINVAL;
+    if (cache->type != DGEN_TYPE_E4M3 && cache->type != type) return DGEN_EINVAL;
+    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads) return DGEN_EINVAL;
+    if (static_cast<int64_t>(n_tokens) * n_q_heads > INT32_MAX) return DGEN_EINVAL;
+    if (!std::isfinite(scale) || !(cap >= 0.f) || std::isinf(cap) || window < 0 || (causal != 0 && causal != 1))
+        return DGEN_EINVAL;
+    if (n_tokens == 0) return DGEN_OK;
+    if (!good_rows(q) || !good_rows(out)) return DGEN_EINVAL;
+    if (!aligned16(workspace)) return DGEN_EINVAL;
+    if (workspace_bytes < static_cast<int64_t>(kCounterBytes)) return DGEN_ESCRATCH;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DGEN_ECUDA;
+    const int sms = sm_count(dev);
+    if (sms < 1) return DGEN_ECUDA;
+    paged::AttendArgs a{};
+    a.c = view(cache, n_tokens, cu);
+    a.q = view(q);
+    a.out = view(out);
+    a.p.G = n_q_heads / cache->n_kv_heads;
+    a.p.causal = causal;
+    a.p.window = window;
+    a.p.rows_min = 1;
+    a.p.rows_max = INT32_MAX;
+    a.lse = lse;
+    a.Hq = n_q_heads;
+    a.scale = scale;
+    a.cap = cap;
+    a.q_bf16 = type == DGEN_TYPE_BF16;
+    a.min_blocks = 2;
+    Workspace ws{static_cast<unsigned int*>(workspace),
+                 reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes),
+                 (static_cast<size_t>(workspace_bytes) - kCounterBytes) / sizeof(float)};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cache->head_dim == 64) return split_hd<64>(st, dev, sms, a, ws, cache->type);
+    if (cache->head_dim == 128) return split_hd<128>(st, dev, sms, a, ws, cache->type);
+    return split_hd<256>(st, dev, sms, a, ws, cache->type);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dgen_paged_append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu_new_dev_or_null, int32_t type,
+                      const dgen_token_rows* k, const dgen_token_rows* v, int32_t n_q_heads,
+                      const dgen_token_rows* q_or_null, const dgen_token_rows* q_out_or_null, float rope_base,
+                      void* stream) {
+    try {
+        return append(cache, n_tokens, cu_new_dev_or_null, type, k, v, n_q_heads, q_or_null, q_out_or_null, rope_base,
+                      stream);
+    } catch (...) {
+        return DGEN_ENOMEM;
+    }
+}
+
+int dgen_paged_attention(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu_new_dev_or_null,
+                         int32_t type, int32_t n_q_heads, const dgen_token_rows* q, const dgen_token_rows* out,
+                         float scale, int32_t causal, int32_t window, float cap, float* lse_dev_or_null,
+                         void* workspace, int64_t workspace_bytes, void* stream) {
+    try {
+        return attend(cache, n_tokens, cu_new_dev_or_null, type, n_q_heads, q, out, scale, causal, window, cap,
+                      lse_dev_or_null, workspace, workspace_bytes, stream);
+    } catch (...) {
+        return DGEN_ENOMEM;
+    }
+}
+
+int64_t dgen_paged_workspace_bytes(void) {
+    // two partial results per CTA of the largest launch (up to 32 rows x (256 + 2) floats each)
+    return static_cast<int64_t>(kCounterBytes) + int64_t{2} * 148 * 2 * 32 * 258 * 4;
+}
+
+}  // extern "C"

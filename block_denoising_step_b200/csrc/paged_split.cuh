@@ -1,0 +1,531 @@
+// Attention of a few query rows per KV head over the paged cache (a sequence's
+// next token, a handful of tokens, or any count where the tcgen05 kernel of
+// paged_block.cuh does not apply).
+//
+//   o = sum_j softmax_j(f(scale q . k_j)) v_j,  f(s) = cap tanh(s / cap) or s
+//
+// One pass over the keys with a running maximum m and sum l per row.  The
+// G query heads of a KV head (times the new tokens) are the rows; they fill the
+// N side (8 per tile) of mma.sync m16n8k16 and the keys the M side, so one token
+// of a group of up to 8 heads wastes nothing that matters: S^T = K Q^T
+// (16 keys x 8 rows per instruction), O^T += V^T P^T.  P^T's operand layout is
+// S^T's accumulator layout transposed 8 x 8 (movmatrix).  P is kept as hi + lo
+// 16-bit parts (about 16 significant bits), so the output's own rounding is the
+// only one that shows.
+//
+// Memory-bound: every visible K and V row is read once.  Each warp streams its
+// own 16-key tiles through a private ring of shared memory (cp.async 16 bytes,
+// XOR-swizzled by row; no block barrier in the loop); the page of each row is
+// looked up per key, one tile ahead, so a page may end anywhere in a tile.  Rows
+// outside the sequence's visible range or without a page are filled with zeros
+// and masked: nothing behind a sequence's end is read.
+//
+// E4M3 caches: bytes are widened to fp16 (exact) in registers; queries are
+// scaled by a power of two per row into fp16's range; the head's scales enter
+// the score factor and the output.  A pair of ldmatrix b16 lanes holds four
+// bytes, so the k order within 16 elements is permuted alike in K and Q.
+#pragma once
+
+#include "mma_sync.cuh"
+#include "paged_work.cuh"
+
+namespace dgen {
+namespace paged {
+
+constexpr int kSplitWarps = 4;
+constexpr int kTileKeys = 16;                        // keys per warp tile
+constexpr int kBlockKeys = kSplitWarps * kTileKeys;  // keys per block of the line
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescale = 8.f;  // the running maximum moves only when it grows by more than 2^8
+
+struct AttendArgs {
+    CacheView c;
+    RowsView q, out;
+    Partition p;
+    float* lse;  // [tokens][Hq] or null
+    int Hq;
+    float scale, cap;
+    int q_bf16;
+    unsigned int* counters;  // [grid]
+    float* parts;            // [2 grid][R][HD] then [2 grid][R][2]
+    int min_blocks;
+};
+
+template <int HD, int ES>
+struct SplitLayout {
+    static constexpr int ROWB = HD * ES;        // bytes of a cache row
+    static constexpr int CH = ROWB / 16;        // 16-byte chunks of a row
+    static constexpr int TILE = kTileKeys * ROWB;
+    static constexpr int STAGES = 3;
+    static constexpr int RING = kSplitWarps * STAGES * 2 * TILE;
+};
+template <int HD, int ES, int NT>
+struct SplitSmem {
+    using L = SplitLayout<HD, ES>;
+    static constexpr int R = 8 * NT;
+    static constexpr int OP = HD + 4;  // padded row of the join buffers
+    static constexpr int JOIN = kSplitWarps * R * OP * 4;
+    static constexpr int Q_OFF = L::RING > JOIN ? L::RING : JOIN;
+    static constexpr int QS_OFF = Q_OFF + R * HD * 2;             // float qscale[R]
+    static constexpr int ML_OFF = QS_OFF + R * 4;                 // float m[W][R], l[W][R]
+    static constexpr int MASK_OFF = ML_OFF + 2 * kSplitWarps * R * 4;  // uint32 mask[W][STAGES]
+    static constexpr int FLAG_OFF = MASK_OFF + kSplitWarps * L::STAGES * 4;
+    static constexpr int BYTES = (FLAG_OFF + 16 + 15) & ~15;
+};
+
+// chunk position of chunk c in row r: eight rows of one chunk column fall into
+// eight different 16-byte bank groups
+template <int CH>
+__device__ __forceinline__ int swz_chunk(int r, int c) {
+    return CH >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <bool BF>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        attn::mma16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two E4M3 bytes (low half of v) -> two fp16 values, exact
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3);
+    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// log2(e) cap tanh(s / cap) from x = 2 log2(e) s / cap, with tanh y = 1 - 2 / (1 + e^2y)
+__device__ __forceinline__ float capped_log2(float x, float cap) {
+    return kLog2e * cap * (1.f - __fdividef(2.f, 1.f + exp2f(x)));
+}
+
+// HD: head size.  ES: bytes of a cache element.  BF: the products run in bf16
+// (else fp16; always fp16 for E4M3 caches).  NT: tiles of 8 query rows.
+template <int HD, int ES, bool BF, int NT>
+__global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const AttendArgs a) {
+    using L = SplitLayout<HD, ES>;
+    using S = SplitSmem<HD, ES, NT>;
+    using H2 = Half2<BF>;
+    constexpr int R = S::R, CH = L::CH, ST = L::STAGES, QCH = HD / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const uint32_t sbase = smem_u32(smem), ring = sbase + warp * (ST * 2 * L::TILE), sq = sbase + S::Q_OFF;
+    float* qscale = reinterpret_cast<float*>(smem + S::QS_OFF);
+    float* s_m = reinterpret_cast<float*>(smem + S::ML_OFF);
+    float* s_l = s_m + kSplitWarps * R;
+    uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + S::MASK_OFF) + warp * ST;
+    int* s_flag = reinterpret_cast<int*>(smem + S::FLAG_OFF);
+    float* join = reinterpret_cast<float*>(smem);
+
+    pdl_enter();
+    const CacheView& c = a.c;
+    Walk walk;
+    walk.start(c, a.p, lane, a.min_blocks);
+    SeqInfo s;
+    int unit, b0, b1;
+    long long u0;
+    while (walk.next(c, a.p, lane, s, unit, b0, b1, u0)) {
+        const int h = unit / s.tiles, rt = unit % s.tiles;
+        const int row0 = rt * R, rows = min(R, s.n * a.p.G - row0);
+        // this tile's own key range within the sequence's
+        const int key_first = s.lo + b0 * kBlockKeys + warp * kTileKeys;
+        const int n_tiles = b1 - b0;
+
+        // rows of the next tile to fetch: table entry loaded one tile ahead
+        int key_next = key_first + (lane & 15);
+        int id_next = key_next < s.hi ? page_entry(c, s.b, key_next / c.page) : -1;
+        auto fetch = [&](int stage, bool live) {
+            uint32_t row = kNoRow;
+            if (live && key_next < s.hi) row = row_in_page(c, id_next, h, key_next % c.page);
+            key_next += kBlockKeys;
+            id_next = live && key_next < s.hi ? page_entry(c, s.b, key_next / c.page) : -1;
+            const uint32_t mask = __ballot_sync(0xffffffffu, row != kNoRow) & 0xFFFFu;
+            if (lane == 0) s_mask[stage] = mask;
+            if (mask != 0) {
+                const uint32_t dk = ring + stage * (2 * L::TILE), dv = dk + L::TILE;
+#pragma unroll
+                for (int i = 0; i < kTileKeys * CH / 32; ++i) {
+                    const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                    const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                    const bool ok = src != kNoRow;
+                    const size_t off = ok ? static_cast<size_t>(src) * L::ROWB + ch * 16 : 0;
+                    const uint32_t d = r * L::ROWB + swz_chunk<CH>(r, ch) * 16;
+                    attn::cp_async16(dk + d, c.k + off, ok);
+                    attn::cp_async16(dv + d, c.v + off, ok);
+                }
+            }
+            attn::cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) fetch(i, i < n_tiles);
+
+        // queries -> shared memory, one warp per row
+        for (int r = warp; r < R; r += kSplitWarps) {
+            constexpr int PER = HD / 32;  // elements per lane: 2, 4 or 8
+            uint32_t w[PER / 2];
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e) w[e] = 0;
+            if (r < rows) {
+                const int tok = s.first + (row0 + r) / a.p.G, head = h * a.p.G + (row0 + r) % a.p.G;
+                const uint8_t* p = a.q.p + (tok * a.q.ts + head * a.q.hs + lane * PER) * 2;
+                if constexpr (PER == 8) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(p);
+                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                } else if constexpr (PER == 4) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(p);
+                    w[0] = v.x, w[1] = v.y;
+                } else {
+                    w[0] = *reinterpret_cast<const uint32_t*>(p);
+                }
+            }
+            if constexpr (ES == 2) {
+                if (lane == 0) qscale[r] = 1.f;
+            } else {  // power-of-two scale into fp16's range, bf16 or fp16 in
+                float2 x[PER / 2];
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < PER / 2; ++e) {
+                    x[e] = a.q_bf16 ? Half2<true>::unpack(w[e]) : Half2<false>::unpack(w[e]);
+                    m = fmaxf(m, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                int ex = 0;
+                if (m > 0.f && m < INFINITY) frexpf(m, &ex);
+                ex = min(max(ex, -100), 100);
+                const float down = ldexpf(1.f, -ex);
+#pragma unroll
+                for (int e = 0; e < PER / 2; ++e) w[e] = Half2<false>::pack(x[e].x * down, x[e].y * down);
+                if (lane == 0) qscale[r] = ldexpf(1.f, ex);
+            }
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e) {
+                int el = lane * PER + 2 * e;  // element pair el, el + 1
+                if constexpr (ES == 1) {
+                    // memory element 4t + 2j + i of a 16-block sits at k = 8j + 2t + i
+                    const int blk = el & ~15, x = el & 15;
+                    el = blk + ((x >> 1) & 1) * 8 + (x >> 2) * 2;
+                }
+                const int ch = el >> 3;
+                *reinterpret_cast<uint32_t*>(smem + S::Q_OFF + r * (HD * 2) + swz_chunk<QCH>(r, ch) * 16 +
+                                             (el & 7) * 2) = w[e];
+            }
+        }
+
+        // visible range and score factor of this thread's rows (columns 2 t4, 2 t4 + 1 of each tile)
+        int vlo[NT][2], vhi[NT][2];
+        int all_lo = 0, all_hi = s.hi;  // keys every row of the tile sees
+        {
+            int lo_l, hi_f, dummy;
+            visible(s.pos0 + row0 / a.p.G, s.len, a.p.causal, a.p.window, dummy, hi_f);
+            visible(s.pos0 + (row0 + rows - 1) / a.p.G, s.len, a.p.causal, a.p.window, lo_l, dummy);
+            all_lo = lo_l;
+            all_hi = hi_f;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = min(nt * 8 + 2 * t4 + j, rows - 1);
+                visible(s.pos0 + (row0 + r) / a.p.G, s.len, a.p.causal, a.p.window, vlo[nt][j], vhi[nt][j]);
+            }
+        __syncthreads();  // queries staged
+        const float kscale = ES == 1 ? __ldg(c.k_scale + h) : 1.f;
+        float fac[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float f = a.scale * kscale * (ES == 1 ? qscale[nt * 8 + 2 * t4 + j] : 1.f);
+                fac[nt][j] = a.cap > 0.f ? f * (2.f * kLog2e / a.cap) : f * kLog2e;
+            }
+
+        float o[HD / 16][NT][4];
+        float m_run[NT][2], l_run[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m_run[nt][0] = m_run[nt][1] = -INFINITY;
+            l_run[nt][0] = l_run[nt][1] = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+        }
+
+        for (int i = 0; i < n_tiles; ++i) {
+            attn::cp_wait<ST - 2>();
+            __syncwarp();
+            const int stage = i % ST;
+            const uint32_t mask = s_mask[stage];
+            const int key0 = key_first + i * kBlockKeys;
+            if (mask != 0) {  // (warp-uniform)
+                const uint32_t tk = ring + stage * (2 * L::TILE), tv = tk + L::TILE;
+                float sc[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+                // S^T = K Q^T, 32 elements of hd per step
+#pragma unroll
+                for (int kk = 0; kk < HD / 32; ++kk) {
+                    uint32_t ka[2][4];
+                    const int r = lane & 15;
+                    if constexpr (ES == 2) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            attn::ldsm_x4(tk + r * L::ROWB + swz_chunk<CH>(r, 4 * kk + 2 * u + (lane >> 4)) * 16,
+                                          ka[u][0], ka[u][1], ka[u][2], ka[u][3]);
+                    } else {
+                        uint32_t x[4];  // keys 0-7 / 8-15 of the first 16 bytes, then of the second
+                        attn::ldsm_x4(tk + r * L::ROWB + swz_chunk<CH>(r, 2 * kk + (lane >> 4)) * 16, x[0], x[1],
+                                      x[2], x[3]);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint32_t v = x[2 * u + half];
+                                ka[u][half] = e4m3x2_f16x2(static_cast<uint16_t>(v));
+                                ka[u][2 + half] = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
+                            }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t b[4];  // k 0-7, 8-15, 16-23, 24-31 of rows nt * 8 ..
+                        const int qr = nt * 8 + (lane & 7);
+                        attn::ldsm_x4(sq + qr * (HD * 2) + swz_chunk<QCH>(qr, 4 * kk + (lane >> 3)) * 16, b[0], b[1],
+                                      b[2], b[3]);
+                        mma_16816<BF>(sc[nt], ka[0], b[0], b[1]);
+                        mma_16816<BF>(sc[nt], ka[1], b[2], b[3]);
+                    }
+                }
+                // log2-domain scores, masks, running maximum
+                const bool full = mask == 0xFFFFu && key0 >= all_lo && key0 + kTileKeys <= all_hi;
+                bool move = false;
+                float mt_[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float x0 = sc[nt][j] * fac[nt][j], x1 = sc[nt][2 + j] * fac[nt][j];
+                        if (a.cap > 0.f) {
+                            x0 = capped_log2(x0, a.cap);
+                            x1 = capped_log2(x1, a.cap);
+                        }
+                        if (!full) {
+                            const int k0 = key0 + g, k1 = k0 + 8;
+                            if (!((mask >> g) & 1u) || k0 < vlo[nt][j] || k0 >= vhi[nt][j]) x0 = -INFINITY;
+                            if (!((mask >> (g + 8)) & 1u) || k1 < vlo[nt][j] || k1 >= vhi[nt][j]) x1 = -INFINITY;
+                        }
+                        sc[nt][j] = x0;
+                        sc[nt][2 + j] = x1;
+                        float mx = fmaxf(x0, x1);
+#pragma unroll
+                        for (int w = 4; w <= 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                        mt_[nt][j] = mx;
+                        move |= mx > m_run[nt][j] + kRescale || (m_run[nt][j] == -INFINITY && mx > -INFINITY);
+                    }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float corr[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float mn = fmaxf(m_run[nt][j], mt_[nt][j]);
+                            corr[j] = m_run[nt][j] == -INFINITY ? 0.f : exp2f(m_run[nt][j] - mn);
+                            m_run[nt][j] = mn;
+                            l_run[nt][j] *= corr[j];
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[mt][nt][e] *= corr[e & 1];
+                    }
+                }
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+                        p[e] = exp2f(sc[nt][e] - mu);
+                        l_run[nt][e & 1] += p[e];
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t hi = H2::pack(p[2 * half], p[2 * half + 1]);
+                        const float2 hf = H2::unpack(hi);
+                        ph[nt][half] = movmatrix_t(hi);
+                        pl[nt][half] = movmatrix_t(H2::pack(p[2 * half] - hf.x, p[2 * half + 1] - hf.y));
+                    }
+                }
+                // O^T += V^T P^T
+                const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+                if constexpr (ES == 2) {
+#pragma unroll
+                    for (int mt = 0; mt < HD / 16; ++mt) {
+                        uint32_t va[4];
+                        attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mt + vc) * 16, va[0], va[1], va[2],
+                                        va[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_16816<BF>(o[mt][nt], va, ph[nt][0], ph[nt][1]);
+                            mma_16816<BF>(o[mt][nt], va, pl[nt][0], pl[nt][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int mp = 0; mp < HD / 32; ++mp) {
+                        uint32_t x[4];  // two 16-byte columns x keys 0-7, then keys 8-15
+                        attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mp + vc) * 16, x[0], x[1], x[2],
+                                        x[3]);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint32_t va[4];
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint32_t v = x[2 * half + u];
+                                const uint32_t e0 = e4m3x2_f16x2(static_cast<uint16_t>(v));
+                                const uint32_t e1 = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
+                                va[2 * half] = __byte_perm(e0, e1, 0x5410);      // byte 2g: row g
+                                va[2 * half + 1] = __byte_perm(e0, e1, 0x7632);  // byte 2g + 1: row g + 8
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_16816<BF>(o[2 * mp + u][nt], va, ph[nt][0], ph[nt][1]);
+                                mma_16816<BF>(o[2 * mp + u][nt], va, pl[nt][0], pl[nt][1]);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // every lane has read stage `stage` and its mask
+            fetch((i + ST - 1) % ST, i + ST - 1 < n_tiles);
+        }
+        attn::cp_wait<0>();
+
+        // join the four warps: m, then scaled O and l
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int w = 4; w <= 16; w <<= 1) l_run[nt][j] += __shfl_xor_sync(0xffffffffu, l_run[nt][j], w);
+                if (g == 0) {
+                    s_m[warp * R + nt * 8 + 2 * t4 + j] = m_run[nt][j];
+                    s_l[warp * R + nt * 8 + 2 * t4 + j] = l_run[nt][j];
+                }
+            }
+        __syncthreads();  // all warps are past their rings
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = nt * 8 + 2 * t4 + j;
+                const float f = m_run[nt][j] == -INFINITY
+                                    ? 0.f
+                                    : exp2f(m_run[nt][j] - fmaxf(fmaxf(s_m[r], s_m[R + r]),
+                                                                 fmaxf(s_m[2 * R + r], s_m[3 * R + r])));
+#pragma unroll
+                for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int col = ES == 2 ? mt * 16 + g + 8 * half : mt * 16 + 2 * g + half;
+                        join[(warp * R + r) * S::OP + col] = o[mt][nt][2 * half + j] * f;
+                    }
+            }
+        __syncthreads();
+        const bool whole = b0 == 0 && b1 == s.blocks;
+        const int slot = 2 * blockIdx.x + (b0 == 0 ? 1 : 0);
+        const size_t n_slots = 2 * static_cast<size_t>(gridDim.x);
+        float* part_o = a.parts;
+        float* part_ml = a.parts + n_slots * R * HD;
+        // merged m and l of row r of this piece
+        auto piece_ml = [&](int r, float& m, float& l) {
+            m = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
+            l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kSplitWarps; ++w)  // (a warp without a maximum has l = 0, or NaN from NaN scores)
+                l += s_l[w * R + r] * (s_m[w * R + r] == -INFINITY ? 1.f : exp2f(s_m[w * R + r] - m));
+        };
+        const float vscale = ES == 1 ? __ldg(c.v_scale + h) : 1.f;
+        auto store = [&](int r, int col, float4 v, float m, float l) {
+            const int tok = s.first + (row0 + r) / a.p.G, head = h * a.p.G + (row0 + r) % a.p.G;
+            const float inv = l > 0.f || l != l ? vscale / l : 0.f;
+            uint2 w;
+            if (ES == 2 ? BF : a.q_bf16 != 0)
+                w = make_uint2(Half2<true>::pack(v.x * inv, v.y * inv), Half2<true>::pack(v.z * inv, v.w * inv));
+            else
+                w = make_uint2(Half2<false>::pack(v.x * inv, v.y * inv), Half2<false>::pack(v.z * inv, v.w * inv));
+            *reinterpret_cast<uint2*>(a.out.p + (tok * a.out.ts + head * a.out.hs + col) * 2) = w;
+            if (a.lse != nullptr && col == 0)
+                a.lse[static_cast<size_t>(tok) * a.Hq + head] =
+                    l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        };
+        for (int i = threadIdx.x; i < rows * (HD / 4); i += kSplitWarps * 32) {
+            const int r = i / (HD / 4), col = (i % (HD / 4)) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kSplitWarps; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(join + (w * R + r) * S::OP + col);
+                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+            float m, l;
+            piece_ml(r, m, l);
+            if (whole) {
+                store(r, col, v, m, l);
+            } else {
+                __stcg(reinterpret_cast<float4*>(part_o + (static_cast<size_t>(slot) * R + r) * HD + col), v);
+                if (col == 0)
+                    __stcg(reinterpret_cast<float2*>(part_ml + (static_cast<size_t>(slot) * R + r) * 2),
+                           make_float2(m, l));
+            }
+        }
+        if (!whole) {
+            const int c_first = static_cast<int>(u0 / walk.per);
+            const int c_last = static_cast<int>((u0 + s.blocks - 1) / walk.per);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0)
+                *s_flag = atomicInc(a.counters + c_first, c_last - c_first) == static_cast<unsigned>(c_last - c_first);
+            __syncthreads();
+            if (*s_flag) {  // every piece of this unit is in memory; the counter is back at zero
+                __threadfence();
+                for (int i = threadIdx.x; i < rows * (HD / 4); i += kSplitWarps * 32) {
+                    const int r = i / (HD / 4), col = (i % (HD / 4)) * 4;
+                    float m = -INFINITY, l = 0.f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = c_first; k <= c_last; ++k) {
+                        const size_t sl = (2 * static_cast<size_t>(k) + (k == c_first ? 1 : 0)) * R + r;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml + sl * 2));
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o + sl * HD + col));
+                        if (ml.x == -INFINITY) {  // no key, or NaN scores alone
+                            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                            l += ml.y;
+                            continue;
+                        }
+                        const float mn = fmaxf(m, ml.x);
+                        const float fo = m == -INFINITY ? 0.f : exp2f(m - mn), fn = exp2f(ml.x - mn);
+                        v.x = v.x * fo + x.x * fn, v.y = v.y * fo + x.y * fn;
+                        v.z = v.z * fo + x.z * fn, v.w = v.w * fo + x.w * fn;
+                        l = l * fo + ml.y * fn;
+                        m = mn;
+                    }
+                    store(r, col, v, m, l);
+                }
+            }
+        }
+        __syncthreads();  // join buffers free before the next unit's copies
+    }
+}
+
+}  // namespace paged
+}  // namespace dgen

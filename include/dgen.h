@@ -449,6 +449,97 @@ int dgen_sample_from_logits_noalloc(const float* logits_dev, int32_t* tok_dev, u
                                     uint64_t seed, float tau_max, float tau_min, int32_t commit_per_step,
                                     float* conf_dev_or_null, void* stream);
 
+/* ---------------------------------------------------------------- paged KV cache
+ * Handle-free operators for serving batches whose sequences have lengths of
+ * their own: a key / value cache in pages, the append of new tokens to it and
+ * the new tokens' attention over it.  (The pages of the method have no
+ * counterpart; the heads, the rotation and the grouping are the decoder's.)
+ *
+ * One layer's cache: keys and values [n_pages][n_kv_heads][page_size][head_dim],
+ * contiguous; page_table[b][p] (row stride table_stride, table_pages entries
+ * used) is the page that holds positions p * page_size .. of sequence b, and
+ * kv_len[b] its length INCLUDING the new tokens of the call, so sequence b's
+ * n_b new tokens sit at positions kv_len[b] - n_b .. kv_len[b] - 1.  Table and
+ * lengths are device memory read when the call runs: a captured call follows
+ * their later contents.  Any page_size; entries of pages behind a sequence's
+ * end are never read.  An entry outside [0, n_pages) is an absent page: rows
+ * for it are not written, keys in it are not attended to (an evicted range).
+ * Pages may be shared by sequences that only read them.
+ *
+ * Token rows are packed: [tokens][heads][head_dim] views whose last dimension is
+ * contiguous and whose strides (in elements) are multiples of 8, the base
+ * 16-byte aligned (e.g. parts of one fused QKV output).  cu_new [batch + 1]
+ * holds each sequence's first row (ascending, cu_new[0] = 0); NULL = n_tokens /
+ * batch rows each.  Sequences may have no new token.  Rows at and behind
+ * cu_new[batch] are padding: neither read nor written.  A new token whose
+ * position would be negative (kv_len < n_b) is not appended.
+ *
+ * type: DGEN_TYPE_BF16 or DGEN_TYPE_F16 of the rows; the cache has the same type
+ * or DGEN_TYPE_E4M3 (OCP FP8) with one fp32 scale per KV head for keys and for
+ * values: value = scale * stored (stored = value / scale, round to nearest even,
+ * saturating).  head_dim 64, 128 or 256; any n_q_heads / n_kv_heads ratio.
+ * Errors: EINVAL (shape, type, alignment), ESCRATCH (workspace too small),
+ * ECUDA.  stream: a cudaStream_t of the current device; asynchronous, no
+ * allocation, no synchronisation; may be captured into a graph. */
+#define DGEN_TYPE_BF16 0
+#define DGEN_TYPE_F16 1
+#define DGEN_TYPE_E4M3 2
+
+typedef struct dgen_paged_cache {
+    void* k_dev;                   /* 16-byte aligned */
+    void* v_dev;
+    const float* k_scale_dev;      /* [n_kv_heads], E4M3 only, else NULL */
+    const float* v_scale_dev;
+    const int32_t* page_table_dev; /* [batch][table_stride] */
+    const int32_t* kv_len_dev;     /* [batch] */
+    int32_t type;
+    int32_t n_pages;               /* n_pages * n_kv_heads * page_size < 2^32 - 1 */
+    int32_t n_kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+    int32_t batch;
+    int32_t table_pages;           /* table_pages * page_size <= 2^30 */
+    int32_t table_stride;
+} dgen_paged_cache;
+
+typedef struct dgen_token_rows {
+    void* dev;
+    int64_t token_stride;
+    int64_t head_stride;
+} dgen_token_rows;
+
+/* Rotates the new tokens' keys (and queries) by their positions and writes keys
+ * and values into their pages: rotate-half pairs (j, j + hd/2), angle
+ * pos * rope_base^(-2j/hd), in fp32 with the angle reduced in fp64, rounded once.
+ * rope_base 0: no rotation.  q_or_null: n_q_heads query rows, rotated into q_out
+ * (may be q itself); NULL (and n_q_heads 0): keys and values only. */
+int dgen_paged_append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu_new_dev_or_null, int32_t type,
+                      const dgen_token_rows* k, const dgen_token_rows* v, int32_t n_q_heads,
+                      const dgen_token_rows* q_or_null, const dgen_token_rows* q_out_or_null, float rope_base,
+                      void* stream);
+
+/* Attention of the new tokens' (rotated) queries over their sequences' cached
+ * keys, the new tokens' own included: per query head (KV head = head /
+ * (n_q_heads / n_kv_heads)) and query at position p,
+ *   out = sum_j softmax_j(f(scale q . k_j)) v_j,   f(s) = cap tanh(s / cap), or s for cap 0,
+ * over the keys j < kv_len with j <= p (causal 1) and |p - j| < window (0: no
+ * window).  A row that sees no key gives zeros.  lse_or_null [tokens][n_q_heads]
+ * fp32 receives the natural log of the softmax's sum (-inf for such a row), with
+ * which results over parts of a context can be joined.  Scores, softmax and sums
+ * are fp32 with P in about 16 bits; the output is rounded once.  Cached values
+ * inside a sequence are taken to be finite; nothing behind its end is used.
+ * workspace: 16-byte aligned device memory of dgen_paged_workspace_bytes(),
+ * zeroed once before its first use (each call leaves its counters at zero);
+ * calls that can overlap on the GPU, replays of captured calls included, each
+ * need one of their own. */
+int dgen_paged_attention(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu_new_dev_or_null,
+                         int32_t type, int32_t n_q_heads, const dgen_token_rows* q, const dgen_token_rows* out,
+                         float scale, int32_t causal, int32_t window, float cap, float* lse_dev_or_null,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace with which every dgen_paged_attention call can run. */
+int64_t dgen_paged_workspace_bytes(void);
+
 /* Diagnostic entry point (exercised by the tests): the same product with E4M3
  * operands (OCP FP8, one byte per element, row-major [M][K] and [N][K]) through
  * the GEMM core's tcgen05 kind::f8f6f4 path, D fp32 [M][N].  K a multiple of 16.
