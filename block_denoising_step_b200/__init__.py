@@ -33,7 +33,7 @@ EXPORTED = ("dgen_create", "dgen_destroy", "dgen_prefill_prompt", "dgen_set_prom
             "dgen_set_flags", "dgen_expert_usage", "dgen_force_routing", "dgen_set_tuning",
             "dgen_generate_block_eb", "dgen_append_canvas", "dgen_generate", "dgen_capture_residual",
             "dgen_gemm_e4m3", "dgen_set_self_cond", "dgen_gemm_bf16_pair", "dgen_paged_append",
-            "dgen_paged_attention", "dgen_paged_workspace_bytes")
+            "dgen_paged_attention", "dgen_paged_workspace_bytes", "dgen_paged_synchronize")
 PROBE_EXPORTED = ("dgen_gemm_rowsum_variant",)
 
 K_QKV, K_ATTENTION, K_OPROJ, K_ROUTER, K_EXPERT_GATE_UP, K_EXPERT_DOWN, K_SHARED_FFN, K_LM_HEAD, K_SAMPLER, \
@@ -112,6 +112,7 @@ _SIGS = {
     "dgen_paged_append": [_P, _I32, _P, _I32, _P, _P, _I32, _P, _P, _F, _P],
     "dgen_paged_attention": [_P, _I32, _P, _I32, _I32, _P, _P, _F, _I32, _I32, _F, _P, _P, _I64, _P],
     "dgen_paged_workspace_bytes": [],
+    "dgen_paged_synchronize": [_P, _P],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -386,4 +387,4 @@ class Denoiser:
         return ms.value, n.value
 
 
-from .paged import PagedCache, paged_append, paged_attention, paged_workspace  # noqa: E402,F401
+from .paged import PagedCache, paged_append, paged_attention, paged_synchronize, paged_workspace  # noqa: E402,F401

@@ -11,14 +11,15 @@
 #include "dgen.h"
 #include "launch.cuh"
 #include "paged_append.cuh"
+#include "paged_block.cuh"
 #include "paged_split.cuh"
 
 using namespace dgen;
 
 namespace {
 
-constexpr int kMaxGrid = 1024;           // CTAs of an attention launch at most (its counters)
-constexpr size_t kCounterBytes = kMaxGrid * sizeof(unsigned int);
+constexpr int kMaxGrid = 1023;           // CTAs of an attention launch at most (its counters)
+constexpr size_t kCounterBytes = (kMaxGrid + 1) * sizeof(unsigned int);  // and the device-side error word
 constexpr int kMaxDevices = 64;
 
 int sm_count(int dev) {
@@ -34,9 +35,10 @@ int sm_count(int dev) {
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// 16-byte access to every row: base and strides
-bool good_rows(const dgen_token_rows* r) {
-    return r && aligned16(r->dev) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+// 16-byte access to every row: base and strides (of dimensions above one)
+bool good_rows(const dgen_token_rows* r, int tokens, int heads) {
+    return r && aligned16(r->dev) && (tokens == 1 || r->token_stride % 8 == 0) &&
+           (heads == 1 || r->head_stride % 8 == 0);
 }
 
 paged::RowsView view(const dgen_token_rows* r) {
@@ -96,6 +98,7 @@ int append_hd(cudaStream_t st, const paged::AppendArgs& a, int per_block, bool b
 
 struct Workspace {
     unsigned int* counters;
+    int* err;
     float* parts;
     size_t floats;
 };
@@ -105,6 +108,7 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     using S = paged::SplitSmem<HD, ES, NT>;
     a.p.R = S::R;
     a.p.KB = paged::kBlockKeys;
+    a.p.align = 1;
     const int per_sm = S::BYTES <= 112 * 1024 ? 2 : 1;
     int64_t grid = std::min(kMaxGrid, sms * per_sm);
     // no more CTAs than blocks of the longest possible line
@@ -140,6 +144,83 @@ int split_hd(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, cons
     return split_rows<HD, 2, false>(st, dev, sms, a, ws);
 }
 
+// Rows per KV head of one sequence above which the tcgen05 kernel takes it.
+constexpr int kBlockMinRows = 32;
+
+// Whether the tcgen05 kernel can take this call's long sequences: 16-bit cache, a
+// group that fits a row tile, pages that TMA boxes of 8 rows or more divide, and
+// rows and coordinates within a tensor map's reach.
+bool block_fits(const dgen_paged_cache* c, const paged::AttendArgs& a) {
+    const int64_t rows = static_cast<int64_t>(c->n_pages) * c->n_kv_heads * c->page_size;
+    return c->type != DGEN_TYPE_E4M3 && a.p.G <= paged::kBlkRows && c->page_size % 8 == 0 && rows <= INT32_MAX &&
+           (a.c.n_tokens == 1 || a.q.ts > 0) && (a.Hq == 1 || a.q.hs > 0);
+}
+
+bool encode_16bit(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box) {
+    const cuuint32_t es[3] = {1, 1, 1};
+    // (bits are copied, not computed with: one 16-bit type serves both)
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD, bool BF>
+int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const Workspace& ws) {
+    using L = paged::BlockLayout<HD>;
+    if (!load_encode()) return DGEN_ECUDA;
+    const int tokens = paged::kBlkRows / a.p.G;  // per row tile
+    a.p.R = tokens * a.p.G;
+    a.p.KB = a.p.align = paged::kBlkKeys;
+    int log2_br = 3;
+    while (log2_br < 7 && a.c.page % (2 << log2_br) == 0) ++log2_br;
+    CUtensorMap tq, tk, tv;
+    {
+        const cuuint64_t ts = a.c.n_tokens > 1 ? a.q.ts * 2 : static_cast<cuuint64_t>(a.Hq) * HD * 2;
+        const cuuint64_t hs = a.Hq > 1 ? a.q.hs * 2 : HD * 2;
+        const cuuint64_t dims[3] = {HD, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.c.n_tokens)};
+        const cuuint64_t strides[2] = {hs, ts};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.p.G), static_cast<cuuint32_t>(tokens)};
+        const cuuint64_t kdims[2] = {HD, static_cast<cuuint64_t>(a.c.n_pages) * a.c.Hkv * a.c.page};
+        const cuuint64_t kstrides[1] = {HD * 2};
+        const cuuint32_t kbox[2] = {64, 1u << log2_br};
+        if (!encode_16bit(&tq, a.q.p, 3, dims, strides, box) || !encode_16bit(&tk, a.c.k, 2, kdims, kstrides, kbox) ||
+            !encode_16bit(&tv, a.c.v, 2, kdims, kstrides, kbox))
+            return DGEN_EINVAL;
+    }
+    const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
+    const int64_t tiles = std::min<int64_t>(rows, rows / a.p.R + a.c.B) * a.c.Hkv;
+    const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + 2 * paged::kBlkKeys - 2) / paged::kBlkKeys;
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), tiles * blocks));
+    if (2 * static_cast<size_t>(grid) * a.p.R * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
+    auto kern = paged::paged_block_kernel<HD, BF>;
+    set_smem_attr_once(kern, L::SMEM_BYTES, dev);
+    a.counters = ws.counters;
+    a.parts = ws.parts;
+    return launch_ex(st, kern, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM_BYTES, tq, tk, tv, a,
+                     log2_br, ws.err) == cudaSuccess
+               ? DGEN_OK
+               : DGEN_ECUDA;
+}
+
+// Sequences with more than kBlockMinRows query rows per KV head go to the tcgen05
+// kernel, the others to the split kernel; a ragged batch may hold both kinds, and
+// each launch passes over the other's.
+template <int HD>
+int attend_hd(cudaStream_t st, int dev, int sms, const dgen_paged_cache* c, paged::AttendArgs a, const Workspace& ws) {
+    const int64_t most = (a.c.cu ? a.c.n_tokens : a.c.n_uniform) * static_cast<int64_t>(a.p.G);
+    const bool block = block_fits(c, a) && most > kBlockMinRows;
+    if (block) {
+        paged::AttendArgs b = a;
+        b.p.rows_min = kBlockMinRows + 1;
+        const int rc = c->type == DGEN_TYPE_BF16 ? launch_block<HD, true>(st, dev, sms, b, ws)
+                                                 : launch_block<HD, false>(st, dev, sms, b, ws);
+        if (rc != DGEN_OK || !a.c.cu) return rc;
+        a.p.rows_max = kBlockMinRows;
+    }
+    return split_hd<HD>(st, dev, sms, a, ws, c->type);
+}
+
 int append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, int32_t type, const dgen_token_rows* k,
            const dgen_token_rows* v, int32_t n_q_heads, const dgen_token_rows* q, const dgen_token_rows* q_out,
            float rope_base, void* stream) {
@@ -149,9 +230,9 @@ int append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (cache->type != DGEN_TYPE_E4M3 && cache->type != type) return DGEN_EINVAL;
     if (n_q_heads < 0 || n_q_heads > 65536 || !(rope_base >= 0.f) || std::isinf(rope_base)) return DGEN_EINVAL;
     if (n_tokens == 0) return DGEN_OK;
-    if (!good_rows(k) || !good_rows(v)) return DGEN_EINVAL;
+    if (!good_rows(k, n_tokens, cache->n_kv_heads) || !good_rows(v, n_tokens, cache->n_kv_heads)) return DGEN_EINVAL;
     if ((n_q_heads > 0) != (q != nullptr) || !q != !q_out) return DGEN_EINVAL;
-    if (q && (!good_rows(q) || !good_rows(q_out))) return DGEN_EINVAL;
+    if (q && (!good_rows(q, n_tokens, n_q_heads) || !good_rows(q_out, n_tokens, n_q_heads))) return DGEN_EINVAL;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DGEN_ECUDA;
     const int sms = sm_count(dev);
@@ -187,7 +268,7 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (!std::isfinite(scale) || !(cap >= 0.f) || std::isinf(cap) || window < 0 || (causal != 0 && causal != 1))
         return DGEN_EINVAL;
     if (n_tokens == 0) return DGEN_OK;
-    if (!good_rows(q) || !good_rows(out)) return DGEN_EINVAL;
+    if (!good_rows(q, n_tokens, n_q_heads) || !good_rows(out, n_tokens, n_q_heads)) return DGEN_EINVAL;
     if (!aligned16(workspace)) return DGEN_EINVAL;
     if (workspace_bytes < static_cast<int64_t>(kCounterBytes)) return DGEN_ESCRATCH;
     int dev = 0;
@@ -209,13 +290,13 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     a.cap = cap;
     a.q_bf16 = type == DGEN_TYPE_BF16;
     a.min_blocks = 2;
-    Workspace ws{static_cast<unsigned int*>(workspace),
+    Workspace ws{static_cast<unsigned int*>(workspace), static_cast<int*>(workspace) + kMaxGrid,
                  reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes),
                  (static_cast<size_t>(workspace_bytes) - kCounterBytes) / sizeof(float)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cache->head_dim == 64) return split_hd<64>(st, dev, sms, a, ws, cache->type);
-    if (cache->head_dim == 128) return split_hd<128>(st, dev, sms, a, ws, cache->type);
-    return split_hd<256>(st, dev, sms, a, ws, cache->type);
+    if (cache->head_dim == 64) return attend_hd<64>(st, dev, sms, cache, a, ws);
+    if (cache->head_dim == 128) return attend_hd<128>(st, dev, sms, cache, a, ws);
+    return attend_hd<256>(st, dev, sms, cache, a, ws);
 }
 
 }  // namespace
@@ -247,8 +328,23 @@ int dgen_paged_attention(const dgen_paged_cache* cache, int32_t n_tokens, const 
 }
 
 int64_t dgen_paged_workspace_bytes(void) {
-    // two partial results per CTA of the largest launch (up to 32 rows x (256 + 2) floats each)
-    return static_cast<int64_t>(kCounterBytes) + int64_t{2} * 148 * 2 * 32 * 258 * 4;
+    // two partial results per CTA of the largest launch (148 CTAs, 128 rows x (256 + 2) floats each)
+    return static_cast<int64_t>(kCounterBytes) + int64_t{2} * 148 * paged::kBlkRows * 258 * 4;
+}
+
+int dgen_paged_synchronize(void* workspace, void* stream) {
+    if (!aligned16(workspace)) return DGEN_EINVAL;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int* word = static_cast<int*>(workspace) + kMaxGrid;
+    int err = 0;
+    if (cudaMemcpyAsync(&err, word, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return DGEN_ECUDA;
+    if (err == 0) return DGEN_OK;
+    // the call that gave up may have left its counters in between
+    if (cudaMemsetAsync(workspace, 0, kCounterBytes, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+        return DGEN_ECUDA;
+    return DGEN_EDEVICE;
 }
 
 }  // extern "C"

@@ -35,21 +35,6 @@ namespace paged {
 constexpr int kSplitWarps = 4;
 constexpr int kTileKeys = 16;                        // keys per warp tile
 constexpr int kBlockKeys = kSplitWarps * kTileKeys;  // keys per block of the line
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescale = 8.f;  // the running maximum moves only when it grows by more than 2^8
-
-struct AttendArgs {
-    CacheView c;
-    RowsView q, out;
-    Partition p;
-    float* lse;  // [tokens][Hq] or null
-    int Hq;
-    float scale, cap;
-    int q_bf16;
-    unsigned int* counters;  // [grid]
-    float* parts;            // [2 grid][R][HD] then [2 grid][R][2]
-    int min_blocks;
-};
 
 template <int HD, int ES>
 struct SplitLayout {
@@ -100,11 +85,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3);
     return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-}
-
-// log2(e) cap tanh(s / cap) from x = 2 log2(e) s / cap, with tanh y = 1 - 2 / (1 + e^2y)
-__device__ __forceinline__ float capped_log2(float x, float cap) {
-    return kLog2e * cap * (1.f - __fdividef(2.f, 1.f + exp2f(x)));
 }
 
 // HD: head size.  ES: bytes of a cache element.  BF: the products run in bf16
@@ -444,49 +424,27 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
             }
         __syncthreads();
         const bool whole = b0 == 0 && b1 == s.blocks;
-        const int slot = 2 * blockIdx.x + (b0 == 0 ? 1 : 0);
-        const size_t n_slots = 2 * static_cast<size_t>(gridDim.x);
-        float* part_o = a.parts;
-        float* part_ml = a.parts + n_slots * R * HD;
-        // merged m and l of row r of this piece
-        auto piece_ml = [&](int r, float& m, float& l) {
-            m = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
-            l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kSplitWarps; ++w)  // (a warp without a maximum has l = 0, or NaN from NaN scores)
-                l += s_l[w * R + r] * (s_m[w * R + r] == -INFINITY ? 1.f : exp2f(s_m[w * R + r] - m));
-        };
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (b0 == 0 ? 1 : 0);
+        const Tile tile{s.first, row0, rows, h};
+        const bool out_bf = ES == 2 ? BF : a.q_bf16 != 0;
         const float vscale = ES == 1 ? __ldg(c.v_scale + h) : 1.f;
-        auto store = [&](int r, int col, float4 v, float m, float l) {
-            const int tok = s.first + (row0 + r) / a.p.G, head = h * a.p.G + (row0 + r) % a.p.G;
-            const float inv = l > 0.f || l != l ? vscale / l : 0.f;
-            uint2 w;
-            if (ES == 2 ? BF : a.q_bf16 != 0)
-                w = make_uint2(Half2<true>::pack(v.x * inv, v.y * inv), Half2<true>::pack(v.z * inv, v.w * inv));
-            else
-                w = make_uint2(Half2<false>::pack(v.x * inv, v.y * inv), Half2<false>::pack(v.z * inv, v.w * inv));
-            *reinterpret_cast<uint2*>(a.out.p + (tok * a.out.ts + head * a.out.hs + col) * 2) = w;
-            if (a.lse != nullptr && col == 0)
-                a.lse[static_cast<size_t>(tok) * a.Hq + head] =
-                    l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        };
         for (int i = threadIdx.x; i < rows * (HD / 4); i += kSplitWarps * 32) {
             const int r = i / (HD / 4), col = (i % (HD / 4)) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float m = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
+            float l = 0.f;
 #pragma unroll
             for (int w = 0; w < kSplitWarps; ++w) {
                 const float4 x = *reinterpret_cast<const float4*>(join + (w * R + r) * S::OP + col);
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                // (a warp without a maximum has l = 0, or NaN from NaN scores)
+                l += s_l[w * R + r] * (s_m[w * R + r] == -INFINITY ? 1.f : exp2f(s_m[w * R + r] - m));
             }
-            float m, l;
-            piece_ml(r, m, l);
             if (whole) {
-                store(r, col, v, m, l);
+                store4(a, tile, out_bf, vscale, r, col, v, m, l);
             } else {
-                __stcg(reinterpret_cast<float4*>(part_o + (static_cast<size_t>(slot) * R + r) * HD + col), v);
-                if (col == 0)
-                    __stcg(reinterpret_cast<float2*>(part_ml + (static_cast<size_t>(slot) * R + r) * 2),
-                           make_float2(m, l));
+                __stcg(reinterpret_cast<float4*>(part_o(a, HD, slot, r) + col), v);
+                if (col == 0) __stcg(reinterpret_cast<float2*>(part_ml(a, HD, slot, r)), make_float2(m, l));
             }
         }
         if (!whole) {
@@ -499,28 +457,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
             __syncthreads();
             if (*s_flag) {  // every piece of this unit is in memory; the counter is back at zero
                 __threadfence();
-                for (int i = threadIdx.x; i < rows * (HD / 4); i += kSplitWarps * 32) {
-                    const int r = i / (HD / 4), col = (i % (HD / 4)) * 4;
-                    float m = -INFINITY, l = 0.f;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = c_first; k <= c_last; ++k) {
-                        const size_t sl = (2 * static_cast<size_t>(k) + (k == c_first ? 1 : 0)) * R + r;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml + sl * 2));
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o + sl * HD + col));
-                        if (ml.x == -INFINITY) {  // no key, or NaN scores alone
-                            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-                            l += ml.y;
-                            continue;
-                        }
-                        const float mn = fmaxf(m, ml.x);
-                        const float fo = m == -INFINITY ? 0.f : exp2f(m - mn), fn = exp2f(ml.x - mn);
-                        v.x = v.x * fo + x.x * fn, v.y = v.y * fo + x.y * fn;
-                        v.z = v.z * fo + x.z * fn, v.w = v.w * fo + x.w * fn;
-                        l = l * fo + ml.y * fn;
-                        m = mn;
-                    }
-                    store(r, col, v, m, l);
-                }
+                join_pieces<HD>(a, tile, out_bf, vscale, c_first, c_last, threadIdx.x, kSplitWarps * 32);
             }
         }
         __syncthreads();  // join buffers free before the next unit's copies

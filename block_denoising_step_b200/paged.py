@@ -68,6 +68,13 @@ def paged_workspace(device=None):
                        device="cuda" if device is None else device)
 
 
+def paged_synchronize(workspace, stream: int | None = None) -> None:
+    """Wait for the stream; raises DgenError (EDEVICE) if a device-side bounded wait ran out in a call with this
+    workspace since the last check."""
+    st = torch.cuda.current_stream(workspace.device).cuda_stream if stream is None else stream
+    _launch("dgen_paged_synchronize", workspace.device, workspace.data_ptr(), st)
+
+
 def _rows(call, cache, name, t, tokens=None, heads=None, dtype=None):
     """The C view of token rows [tokens][heads][head_dim]."""
     _need(t.dim() == 3 and t.shape[2] == cache.head_dim and t.dtype in _ROW_TYPES and t.device == cache.device, call,
@@ -76,8 +83,7 @@ def _rows(call, cache, name, t, tokens=None, heads=None, dtype=None):
           (dtype is None or t.dtype == dtype), call, f"{name}: shape {tuple(t.shape)} or {t.dtype} does not fit")
     st, sh, se = t.stride()
     _need(se == 1, call, f"{name}: the last dimension must be contiguous")
-    # strides of dimensions of one element are never used
-    return TokenRows(t.data_ptr(), st if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0)
+    return TokenRows(t.data_ptr(), st, sh)
 
 
 def _common(call, cache, rows, cu_new, stream):

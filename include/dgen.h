@@ -526,7 +526,9 @@ int dgen_paged_append(const dgen_paged_cache* cache, int32_t n_tokens, const int
  * window).  A row that sees no key gives zeros.  lse_or_null [tokens][n_q_heads]
  * fp32 receives the natural log of the softmax's sum (-inf for such a row), with
  * which results over parts of a context can be joined.  Scores, softmax and sums
- * are fp32 with P in about 16 bits; the output is rounded once.  Cached values
+ * are fp32; the weights P enter the second product in about 16 bits (up to 32
+ * query rows per KV head and for E4M3 caches) or rounded once to the row type; the
+ * output is rounded once.  Cached values
  * inside a sequence are taken to be finite; nothing behind its end is used.
  * workspace: 16-byte aligned device memory of dgen_paged_workspace_bytes(),
  * zeroed once before its first use (each call leaves its counters at zero);
@@ -539,6 +541,12 @@ int dgen_paged_attention(const dgen_paged_cache* cache, int32_t n_tokens, const 
 
 /* Bytes of workspace with which every dgen_paged_attention call can run. */
 int64_t dgen_paged_workspace_bytes(void);
+
+/* Waits for the stream; DGEN_EDEVICE if a device-side bounded wait ran out in a
+ * dgen_paged_attention call with this workspace since the last check (its outputs
+ * are then not valid; the workspace is put back to its first state), DGEN_ECUDA
+ * on a CUDA error, else DGEN_OK. */
+int dgen_paged_synchronize(void* workspace, void* stream);
 
 /* Diagnostic entry point (exercised by the tests): the same product with E4M3
  * operands (OCP FP8, one byte per element, row-major [M][K] and [N][K]) through

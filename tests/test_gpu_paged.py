@@ -371,6 +371,19 @@ def test_two_streams_at_once_with_a_workspace_each():
         assert ((outs[i].double() - want).abs() <= ref.half_step(torch.bfloat16, want) * 1.01 + slack).all()
 
 
+def test_workspace_status(workspace):
+    """No wait ran out so far; a recorded device error is reported once and the workspace put back."""
+    dg.paged_synchronize(workspace)
+    ws = dg.paged_workspace()
+    ws[:4096].view(torch.int32)[1023] = 5
+    ws[:4096].view(torch.int32)[0] = 3
+    with pytest.raises(dg.DgenError) as e:
+        dg.paged_synchronize(ws)
+    assert e.value.status == dg.DGEN_EDEVICE
+    dg.paged_synchronize(ws)
+    assert not ws[:4096].any()
+
+
 @pytest.mark.parametrize("new", [1, 100])
 def test_same_call_same_bits(new, workspace):
     cache = make_cache("bf16", [5000, 700, 2300], 2, 128, 16, seed=50)

@@ -69,6 +69,18 @@ def test_small_workspace_is_refused():
     assert _attend(ws_bytes=16) == dg.DGEN_ESCRATCH
 
 
+def test_synchronize_refuses_a_bad_workspace():
+    assert dg._lib.dgen_paged_synchronize(None, None) == dg.DGEN_EINVAL
+    assert dg._lib.dgen_paged_synchronize(A + 4, None) == dg.DGEN_EINVAL
+
+
+def test_strides_of_single_rows_do_not_matter():
+    one = _cache(batch=1, n_kv_heads=1)
+    r = _rows(ts=3, hs=5)
+    assert _append(one, n=1, k=r, v=r, heads=1, q=r, q_out=_rows(None, 3, 5)) == dg.DGEN_EINVAL  # for the null alone
+    assert _attend(one, n=1, heads=1, q=r, out=r, ws_bytes=16) == dg.DGEN_ESCRATCH
+
+
 def test_no_tokens_is_nothing_to_do():
     assert _append(n=0) == dg.DGEN_OK
     assert _attend(n=0) == dg.DGEN_OK
