@@ -20,7 +20,10 @@ namespace {
 
 constexpr int kMaxGrid = 1023;           // CTAs of an attention launch at most (its counters)
 constexpr size_t kCounterBytes = (kMaxGrid + 1) * sizeof(unsigned int);  // and the device-side error word
+constexpr size_t kHeadBytes = kCounterBytes + kMaxGrid * 64;             // and the block kernel's join list
+static_assert(sizeof(paged::Piece) <= 64, "join list");
 constexpr int kMaxDevices = 64;
+constexpr int kMaxSplitCtas = 4;         // CTAs per SM of the split kernel at most
 
 int sm_count(int dev) {
     static std::atomic<int> known[kMaxDevices];
@@ -99,28 +102,38 @@ int append_hd(cudaStream_t st, const paged::AppendArgs& a, int per_block, bool b
 struct Workspace {
     unsigned int* counters;
     int* err;
+    paged::Piece* joins;
     float* parts;
     size_t floats;
 };
 
 template <int HD, int ES, bool BF, int NT>
-int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const Workspace& ws) {
+int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const Workspace& ws, int64_t rows_most) {
     using S = paged::SplitSmem<HD, ES, NT>;
     a.p.R = S::R;
-    a.p.KB = paged::kBlockKeys;
-    a.p.align = 1;
-    const int per_sm = S::BYTES <= 112 * 1024 ? 2 : 1;
-    int64_t grid = std::min(kMaxGrid, sms * per_sm);
+    a.p.KB = paged::SplitLayout<HD, ES, NT>::BLOCK_KEYS;
+    a.p.align = rows_most <= S::R ? 1 : a.p.KB;
+    a.p.TS = 1;
+    auto kern = paged::paged_split_kernel<HD, ES, BF, NT>;
+    set_smem_attr_once(kern, S::BYTES, dev);
+    static std::atomic<int> per_sm{0};  // resident CTAs per SM: a property of the kernel
+    if (per_sm.load(std::memory_order_relaxed) == 0) {
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, paged::kSplitWarps * 32, S::BYTES) != cudaSuccess)
+            return DGEN_ECUDA;
+        per_sm.store(std::clamp(n, 1, kMaxSplitCtas), std::memory_order_relaxed);
+    }
+    int64_t grid = std::min(kMaxGrid, sms * per_sm.load(std::memory_order_relaxed));
     // no more CTAs than blocks of the longest possible line
     const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
     const int64_t tiles = std::min<int64_t>(rows, rows / S::R + a.c.B) * a.c.Hkv;
-    const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + paged::kBlockKeys - 1) / paged::kBlockKeys;
-    if (tiles < grid && tiles * blocks < grid) grid = std::max<int64_t>(1, tiles * blocks);
+    const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + a.p.KB - 1) / a.p.KB;
+    if (tiles * blocks >= INT32_MAX) return DGEN_EINVAL;  // (rows <= 2^31, blocks <= 2^24: no overflow)
+    grid = std::max<int64_t>(1, std::min(grid, tiles * blocks));
     if (2 * static_cast<size_t>(grid) * S::R * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
-    auto kern = paged::paged_split_kernel<HD, ES, BF, NT>;
-    set_smem_attr_once(kern, S::BYTES, dev);
     a.counters = ws.counters;
     a.parts = ws.parts;
+    a.n_ctas = static_cast<int>(grid);
     return launch_ex(st, kern, dim3(static_cast<unsigned>(grid)), dim3(paged::kSplitWarps * 32), S::BYTES, a) == cudaSuccess
                ? DGEN_OK
                : DGEN_ECUDA;
@@ -129,19 +142,20 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
 // Row tiles of 8, 16 or (hd <= 128: the accumulators of 32 rows of 256 would not
 // fit the registers) 32 query rows, by the rows a sequence has on average.
 template <int HD, int ES, bool BF>
-int split_rows(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, const Workspace& ws) {
+int split_rows(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, const Workspace& ws, int64_t most) {
     const int64_t rows = (static_cast<int64_t>(a.c.n_tokens) + a.c.B - 1) / a.c.B * a.p.G;
-    if (rows <= 8) return launch_split<HD, ES, BF, 1>(st, dev, sms, a, ws);
+    if (rows <= 8) return launch_split<HD, ES, BF, 1>(st, dev, sms, a, ws, most);
     if constexpr (HD <= 128)
-        if (rows > 16) return launch_split<HD, ES, BF, 4>(st, dev, sms, a, ws);
-    return launch_split<HD, ES, BF, 2>(st, dev, sms, a, ws);
+        if (rows > 16) return launch_split<HD, ES, BF, 4>(st, dev, sms, a, ws, most);
+    return launch_split<HD, ES, BF, 2>(st, dev, sms, a, ws, most);
 }
 
 template <int HD>
-int split_hd(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, const Workspace& ws, int cache_type) {
-    if (cache_type == DGEN_TYPE_E4M3) return split_rows<HD, 1, false>(st, dev, sms, a, ws);
-    if (cache_type == DGEN_TYPE_BF16) return split_rows<HD, 2, true>(st, dev, sms, a, ws);
-    return split_rows<HD, 2, false>(st, dev, sms, a, ws);
+int split_hd(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, const Workspace& ws, int cache_type,
+             int64_t most) {
+    if (cache_type == DGEN_TYPE_E4M3) return split_rows<HD, 1, false>(st, dev, sms, a, ws, most);
+    if (cache_type == DGEN_TYPE_BF16) return split_rows<HD, 2, true>(st, dev, sms, a, ws, most);
+    return split_rows<HD, 2, false>(st, dev, sms, a, ws, most);
 }
 
 // Rows per KV head of one sequence above which the tcgen05 kernel takes it.
@@ -188,17 +202,28 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
             !encode_16bit(&tv, a.c.v, 2, kdims, kstrides, kbox))
             return DGEN_EINVAL;
     }
+    // teams of 4 or 2 row tiles where the average sequence's tiles fill them to 7/8
     const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
-    const int64_t tiles = std::min<int64_t>(rows, rows / a.p.R + a.c.B) * a.c.Hkv;
+    const int64_t avg = std::max<int64_t>(1, (rows / a.c.B + a.p.R - 1) / a.p.R);
+    a.p.TS = 1;
+    for (int ts : {4, 2})
+        if (a.p.TS == 1 && 8 * avg >= 7 * ((avg + ts - 1) / ts * ts)) a.p.TS = ts;
+    const int64_t units = std::min<int64_t>(rows, rows / (a.p.R * a.p.TS) + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + 2 * paged::kBlkKeys - 2) / paged::kBlkKeys;
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), tiles * blocks));
-    if (2 * static_cast<size_t>(grid) * a.p.R * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
-    auto kern = paged::paged_block_kernel<HD, BF>;
+    if (units * blocks >= INT32_MAX) return DGEN_EINVAL;
+    const int64_t teams = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid) / a.p.TS, units * blocks));
+    const int64_t grid = teams * a.p.TS;
+    if (2 * static_cast<size_t>(grid) * paged::kBlkRows * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
+    auto kern = a.cap > 0.f ? paged::paged_block_kernel<HD, BF, true> : paged::paged_block_kernel<HD, BF, false>;
+    a.joins = ws.joins;
     set_smem_attr_once(kern, L::SMEM_BYTES, dev);
-    a.counters = ws.counters;
     a.parts = ws.parts;
-    return launch_ex(st, kern, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM_BYTES, tq, tk, tv, a,
-                     log2_br, ws.err) == cudaSuccess
+    a.n_ctas = static_cast<int>(grid);
+    if (launch_ex(st, kern, dim3(a.n_ctas), dim3(L::THREADS), L::SMEM_BYTES, tq, tk, tv, a, log2_br, ws.err) !=
+        cudaSuccess)
+        return DGEN_ECUDA;
+    if (teams == 1) return DGEN_OK;
+    return launch_ex(st, paged::paged_block_join_kernel<HD, BF>, dim3(a.n_ctas, HD / paged::kJoinCols), dim3(256), 0, a) == cudaSuccess
                ? DGEN_OK
                : DGEN_ECUDA;
 }
@@ -208,7 +233,9 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
 // each launch passes over the other's.
 template <int HD>
 int attend_hd(cudaStream_t st, int dev, int sms, const dgen_paged_cache* c, paged::AttendArgs a, const Workspace& ws) {
-    const int64_t most = (a.c.cu ? a.c.n_tokens : a.c.n_uniform) * static_cast<int64_t>(a.p.G);
+    // the most rows one sequence has if none is without a new token (where some are, the split kernel also
+    // takes longer ones): a decode batch given with cu_new costs no second launch
+    const int64_t most = (a.c.cu ? std::max(a.c.n_tokens - a.c.B + 1, 1) : a.c.n_uniform) * static_cast<int64_t>(a.p.G);
     const bool block = block_fits(c, a) && most > kBlockMinRows;
     if (block) {
         paged::AttendArgs b = a;
@@ -218,7 +245,7 @@ int attend_hd(cudaStream_t st, int dev, int sms, const dgen_paged_cache* c, page
         if (rc != DGEN_OK || !a.c.cu) return rc;
         a.p.rows_max = kBlockMinRows;
     }
-    return split_hd<HD>(st, dev, sms, a, ws, c->type);
+    return split_hd<HD>(st, dev, sms, a, ws, c->type, std::min<int64_t>(most, a.p.rows_max));
 }
 
 int append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, int32_t type, const dgen_token_rows* k,
@@ -265,12 +292,12 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (cache->type != DGEN_TYPE_E4M3 && cache->type != type) return DGEN_EINVAL;
     if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads) return DGEN_EINVAL;
     if (static_cast<int64_t>(n_tokens) * n_q_heads > INT32_MAX) return DGEN_EINVAL;
-    if (!std::isfinite(scale) || !(cap >= 0.f) || std::isinf(cap) || window < 0 || (causal != 0 && causal != 1))
+    if (!std::isfinite(scale) || !(scale > 0.f) || !(cap >= 0.f) || std::isinf(cap) || window < 0 || (causal != 0 && causal != 1))
         return DGEN_EINVAL;
     if (n_tokens == 0) return DGEN_OK;
     if (!good_rows(q, n_tokens, n_q_heads) || !good_rows(out, n_tokens, n_q_heads)) return DGEN_EINVAL;
     if (!aligned16(workspace)) return DGEN_EINVAL;
-    if (workspace_bytes < static_cast<int64_t>(kCounterBytes)) return DGEN_ESCRATCH;
+    if (workspace_bytes < static_cast<int64_t>(kHeadBytes)) return DGEN_ESCRATCH;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DGEN_ECUDA;
     const int sms = sm_count(dev);
@@ -291,8 +318,9 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     a.q_bf16 = type == DGEN_TYPE_BF16;
     a.min_blocks = 2;
     Workspace ws{static_cast<unsigned int*>(workspace), static_cast<int*>(workspace) + kMaxGrid,
-                 reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes),
-                 (static_cast<size_t>(workspace_bytes) - kCounterBytes) / sizeof(float)};
+                 reinterpret_cast<paged::Piece*>(static_cast<uint8_t*>(workspace) + kCounterBytes),
+                 reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeadBytes),
+                 (static_cast<size_t>(workspace_bytes) - kHeadBytes) / sizeof(float)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (cache->head_dim == 64) return attend_hd<64>(st, dev, sms, cache, a, ws);
     if (cache->head_dim == 128) return attend_hd<128>(st, dev, sms, cache, a, ws);
@@ -329,7 +357,7 @@ int dgen_paged_attention(const dgen_paged_cache* cache, int32_t n_tokens, const 
 
 int64_t dgen_paged_workspace_bytes(void) {
     // two partial results per CTA of the largest launch (148 CTAs, 128 rows x (256 + 2) floats each)
-    return static_cast<int64_t>(kCounterBytes) + int64_t{2} * 148 * paged::kBlkRows * 258 * 4;
+    return static_cast<int64_t>(kHeadBytes) + int64_t{2} * 148 * paged::kBlkRows * 258 * 4;
 }
 
 int dgen_paged_synchronize(void* workspace, void* stream) {

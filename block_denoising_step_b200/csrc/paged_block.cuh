@@ -6,12 +6,14 @@
 // 128, so K and V are read once for the whole group.  One CTA per SM walks the
 // units of paged_work.cuh in blocks of 128 keys:
 //
+//   warp 2           scheduler: walks the units and hands each piece to the other
+//                    warps through shared memory, two in flight (warp 3 is idle);
 //   warp 0           producer: Q by one TMA box per 64 columns ([tokens][G] rows),
 //                    K and V in stages of 128 keys x SC columns (32 KB), one TMA box
 //                    per page part (BR rows, a power of two that divides the page
 //                    size) and 64 columns, each lane issuing its own box;
 //   warp 1           MMA issuer: S = Q K^T (128 x 128 fp32) into one of two TMEM
-//                    buffers, O += P V with P from tensor memory (the low 64 columns
+//                    buffers, O += P V with P from tensor memory (the upper 64 columns
 //                    of its S buffer) and V MN-major from shared memory;
 //   4 or 8 warps     softmax: thread = query row.  One warpgroup takes every
 //                    tile at hd 256, where O fills half the tensor memory and the
@@ -38,7 +40,7 @@
 namespace dgen {
 namespace paged {
 
-enum : int { ERR_BLOCK_PRODUCER = 20, ERR_BLOCK_MMA = 21, ERR_BLOCK_SOFTMAX = 22, ERR_BLOCK_DRAIN = 23 };
+enum : int { ERR_BLOCK_PRODUCER = 20, ERR_BLOCK_MMA = 21, ERR_BLOCK_SOFTMAX = 22, ERR_BLOCK_DRAIN = 23, ERR_BLOCK_PIECE = 24 };
 
 constexpr int kBlkKeys = 128;
 constexpr int kBlkRows = 128;
@@ -48,16 +50,18 @@ struct BlockLayout {
     static constexpr int SC = HD < 128 ? HD : 128;    // columns of a stage
     static constexpr int NS = HD / SC;                // stages per K or V tile
     static constexpr int NG = HD == 256 ? 1 : 2;      // softmax warpgroups
-    static constexpr int THREADS = 64 + NG * 128;
+    static constexpr int THREADS = 128 + NG * 128;
     static constexpr int Q_BYTES = kBlkRows * HD * 2; // HD / 64 boxes of [128 rows x 128 B]
     static constexpr int STAGE = kBlkKeys * SC * 2;   // SC / 64 boxes of [128 rows x 128 B]
     static constexpr int STAGES = HD == 256 ? 5 : (HD == 128 ? 5 : 8);
     static constexpr int KV_OFF = Q_BYTES;
-    static constexpr int ML_OFF = KV_OFF + STAGES * STAGE;           // float2 ml[NG][128]
-    static constexpr int BAR_OFF = ML_OFF + NG * kBlkRows * 8;
-    // q_full, q_empty, kv_full[ST], kv_empty[ST], s_full[2], p_full[2], pv_done[2], o_free, drain
-    static constexpr int N_BARS = 2 + 2 * STAGES + 6 + 2;
-    static constexpr int SLOT_OFF = BAR_OFF + N_BARS * 8;            // TMEM base, join flag
+    static constexpr int ML_OFF = KV_OFF + STAGES * STAGE;           // float2 ml[2][NG][128]: by unit parity
+    static constexpr int PIECE_OFF = ML_OFF + (NG == 2 ? 2 * NG * kBlkRows * 8 : 0);
+    static constexpr int BAR_OFF = PIECE_OFF + 2 * 64;
+    // q_full, q_empty, kv_full[ST], kv_empty[ST], s_full[2], p_full[2], pv_done[2], o_free, drain, ml_full,
+    // piece_full[2], piece_empty[2]
+    static constexpr int N_BARS = 2 + 2 * STAGES + 6 + 2 + 1 + 4;
+    static constexpr int SLOT_OFF = BAR_OFF + N_BARS * 8;            // TMEM base
     static constexpr int SMEM_BYTES = SLOT_OFF + 16 + 1024;          // + slack for 1024-byte alignment
     static constexpr int T_S = NG * HD;                              // first S column
     static_assert(T_S + 2 * kBlkKeys <= 512, "tensor memory");
@@ -71,28 +75,118 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// D (TMEM) (+)= A (TMEM, K-major, two 16-bit values per column) x B (shared-memory descriptor)
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// The MMA warp stays converged and `issue` (set in one lane) predicates the
+// instructions themselves, so that the descriptors live in uniform registers:
+// issued from inside a one-lane branch, each product took 80 cycles of register
+// moves, more than its 64 on the tensor cores.
+// D (TMEM) (+)= A (shared memory) B^T (shared memory)
+__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
         : "memory");
 }
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// D (TMEM) (+)= A (TMEM, K-major, two 16-bit values per column) x B (shared-memory descriptor)
+__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t issue, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(issue)
+        : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 32 lanes x 16 consecutive fp32 columns from registers
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// C scores of each of this warp's rows
+template <int C>
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&x)[C]) {
+#pragma unroll
+    for (int e = 0; e < C; e += 32) tmem_ld32(taddr + e, reinterpret_cast<uint32_t(&)[32]>(x[e]));
+    tmem_ld_wait();
+}
+// two fp32 values in one register pair: packed arithmetic halves the instructions
+// of the softmax, which shares its issue slots with the exponentials
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // bits [lo, hi) of a 32-bit word whose bit 0 is position `base`
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int base) {
     const int a = min(max(lo - base, 0), 32), b = min(max(hi - base, 0), 32);
     const uint32_t up = b >= 32 ? 0xFFFFFFFFu : (1u << b) - 1u, dn = a >= 32 ? 0xFFFFFFFFu : (1u << a) - 1u;
     return up & ~dn;
+}
+
+// Masks C scores of the tile's columns c0 .. (keys k0 ..): outside [lo, hi), or in
+// an absent page part.
+template <int C>
+__device__ __forceinline__ void mask_scores(float (&x)[C], int lo, int hi, int k0, int c0, uint32_t have, int log2_br) {
+#pragma unroll
+    for (int q = 0; q < C; q += 32) {
+        uint32_t parts = 0;
+        if (log2_br >= 5) {
+            parts = (have >> ((c0 + q) >> log2_br)) & 1u ? 0xFFFFFFFFu : 0u;
+        } else {
+            const uint32_t one = (1u << (1 << log2_br)) - 1u;
+            for (int e = 0; e < 32; e += 1 << log2_br) parts |= (have >> ((c0 + q + e) >> log2_br)) & 1u ? one << e : 0u;
+        }
+        const uint32_t bits = range_bits(lo, hi, k0 + q) & parts;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (!((bits >> e) & 1u)) x[q + e] = -INFINITY;
+    }
+}
+
+// Partial results of this kernel: [slot][hd / 4][128 rows] float4, so that a warp
+// (32 rows) writes and reads whole lines, then [slot][128] (m, l).
+__device__ __forceinline__ float4* block_part(const AttendArgs& a, int hd, size_t slot, int col, int row) {
+    return reinterpret_cast<float4*>(a.parts) + (slot * (hd / 4) + col / 4) * kBlkRows + row;
+}
+__device__ __forceinline__ float2* block_part_ml(const AttendArgs& a, int hd, size_t slot, int row) {
+    return reinterpret_cast<float2*>(a.parts + 2 * static_cast<size_t>(a.n_ctas) * kBlkRows * hd) + slot * kBlkRows + row;
 }
 
 // Page parts of a tile of 128 keys: lane i < nbox holds the cache row of part i
@@ -103,12 +197,15 @@ struct Parts {
         key = key_;
         id = lane < nbox && key < hi ? page_entry(c, b, key / c.page) : -1;
     }
+    __device__ __forceinline__ bool valid(const CacheView& c) const {
+        return static_cast<uint32_t>(id) < static_cast<uint32_t>(c.n_pages);
+    }
     __device__ __forceinline__ uint32_t row(const CacheView& c, int h) const {
         return id >= 0 ? row_in_page(c, id, h, key % c.page) : kNoRow;
     }
 };
 
-template <int HD, bool BF>
+template <int HD, bool BF, bool CAP>
 __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     paged_block_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const AttendArgs a, int log2_br, int* __restrict__ err) {
@@ -122,9 +219,10 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + ST;
     uint64_t *s_full = kv_empty + ST, *p_full = s_full + 2, *pv_done = p_full + 2, *o_free = pv_done + 2,
-             *drain = o_free + 1;
+             *drain = o_free + 1, *ml_full = drain + 1, *piece_full = ml_full + 1, *piece_empty = piece_full + 2;
+    static_assert(sizeof(Piece) <= 64, "piece slot");
+    volatile Piece* s_piece = reinterpret_cast<volatile Piece*>(smem + L::PIECE_OFF);  // 64 bytes apart
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
-    int* s_flag = reinterpret_cast<int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -141,6 +239,11 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         }
         mbar_init(o_free, 4 * NG);
         mbar_init(drain, 1);
+        mbar_init(ml_full, 4 * NG);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&piece_full[i], 1);
+            mbar_init(&piece_empty[i], 2 + 4 * NG);
+        }
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -155,13 +258,49 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     const CacheView& c = a.c;
     const int br = 1 << log2_br, nbox = kBlkKeys >> log2_br;
 
-    Walk walk;
-    walk.start(c, a.p, lane, a.min_blocks);
-    SeqInfo s;
-    int unit, b0, b1;
-    long long u0;
+    Piece s;
+    int piece_no = 0;
+    // The next piece of the scheduler's walk into s; false at its end or when the wait ran out.
+    auto next_piece = [&]() -> bool {
+        const int i = piece_no & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&piece_full[i], (piece_no >> 1) & 1, err, ERR_BLOCK_PIECE))) return false;
+        const volatile int* from = reinterpret_cast<const volatile int*>(reinterpret_cast<const volatile uint8_t*>(s_piece) + i * 64);
+        int* to = reinterpret_cast<int*>(&s);
+#pragma unroll
+        for (int e = 0; e < static_cast<int>(sizeof(Piece) / 4); ++e) to[e] = from[e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_empty[i]);
+        ++piece_no;
+        return s.end == 0;
+    };
 
-    if (warp == 0) {
+    if (warp == 2) {
+        Walk walk;
+        walk.start(c, a.p, lane, a.min_blocks, blockIdx.x, a.n_ctas);
+        bool cut = false;
+        for (int i = 0;; ++i) {
+            Piece q{};
+            const bool have = walk.next(c, a.p, lane, q);
+            q.end = !have;
+            // what the join kernel has to know of the unit that starts here and goes on behind
+            if (lane == 0 && (!have || (q.starts && !q.whole && q.rows > 0))) {
+                if (have || !cut) a.joins[blockIdx.x] = q;
+                cut = true;
+            }
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(&piece_empty[i & 1], ((i >> 1) & 1) ^ 1, err, ERR_BLOCK_PIECE)))
+                break;
+            if (lane == 0) {
+                volatile int* to = reinterpret_cast<volatile int*>(reinterpret_cast<volatile uint8_t*>(s_piece) + (i & 1) * 64);
+                const int* from = reinterpret_cast<const int*>(&q);
+#pragma unroll
+                for (int e = 0; e < static_cast<int>(sizeof(Piece) / 4); ++e) to[e] = from[e];
+                mbar_arrive(&piece_full[i & 1]);
+            }
+            __syncwarp();
+            if (!have) break;
+        }
+    } else if (warp == 0) {
         if (lane == 0) {
             prefetch_tmap(&tmQ);
             prefetch_tmap(&tmK);
@@ -196,16 +335,17 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 }
             }
         };
-        while (ok && walk.next(c, a.p, lane, s, unit, b0, b1, u0)) {
-            const int h = unit / s.tiles, rt = unit % s.tiles, n = b1 - b0;
-            const int key0 = s.lo + b0 * kBlkKeys + lane * br;
+        while (ok && next_piece()) {
+            const int h = s.h, n = s.n;
+            if (n == 0) continue;
+            const int key0 = s.key0 + lane * br;
             if (unit_no > 0 &&
                 !__all_sync(0xffffffffu, mbar_wait(q_empty, (unit_no - 1) & 1, err, ERR_BLOCK_PRODUCER))) {
                 ok = false;
                 break;
             }
             if (lane == 0) {
-                const int tok = s.first + rt * (a.p.R / a.p.G);
+                const int tok = s.first + s.row0 / a.p.G;
                 mbar_expect_tx(q_full, a.p.R * HD * 2);
 #pragma unroll
                 for (int x = 0; x < HD / 64; ++x)
@@ -239,6 +379,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         constexpr uint32_t base = (1u << 4) | type | (static_cast<uint32_t>(kBlkRows >> 4) << 24);
         constexpr uint32_t idesc_s = base | (static_cast<uint32_t>(kBlkKeys >> 3) << 17);
         constexpr uint32_t idesc_pv = base | (1u << 16) | (static_cast<uint32_t>(L::SC >> 3) << 17);
+        const uint32_t issue = lane == 0 ? 1u : 0u;
         int st = 0, unit_no = 0, jj = 0;  // jj: tile counter of the CTA
         uint32_t ph = 0;
         bool ok = true;
@@ -252,9 +393,9 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             }
             return true;
         };
-        while (ok && walk.next(c, a.p, lane, s, unit, b0, b1, u0)) {
-            const int h = unit / s.tiles, n = b1 - b0;
-            const int key0 = s.lo + b0 * kBlkKeys;
+        while (ok && next_piece()) {
+            const int n = s.n, key0 = s.key0;
+            if (n == 0) continue;
             Parts pv;
             pv.ahead(c, s.b, key0 + lane * br, s.hi, nbox, lane);
             if (!__all_sync(0xffffffffu, mbar_wait(q_full, unit_no & 1, err, ERR_BLOCK_MMA))) break;
@@ -265,31 +406,24 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 for (int x = 0; x < L::NS; ++x) {
                     int stage;
                     if (!take(stage)) return false;
-                    if (lane == 0) {
-                        const uint32_t sk = sKV + stage * L::STAGE;
+                    const uint64_t ad0 = sdesc_sw128(sQ + x * (L::SC / 64) * (kBlkRows * 128));
+                    const uint64_t bd0 = sdesc_sw128(sKV + stage * L::STAGE);
 #pragma unroll
-                        for (int kk = 0; kk < L::SC / 16; ++kk) {
-                            const uint64_t ad =
-                                sdesc_sw128(sQ + (x * (L::SC / 64) + (kk >> 2)) * (kBlkRows * 128)) + 2 * (kk & 3);
-                            const uint64_t bd = sdesc_sw128(sk + (kk >> 2) * (kBlkKeys * 128)) + 2 * (kk & 3);
-                            mma_bf16_ss(t_s + buf * kBlkKeys, ad, bd, idesc_s, x > 0 || kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit(smem_u32(&kv_empty[stage]));
+                    for (int kk = 0; kk < L::SC / 16; ++kk) {
+                        const int off = (kk >> 2) * (kBlkRows * 128 / 16) + 2 * (kk & 3);  // 16-byte units
+                        mma_ss(issue, t_s + buf * kBlkKeys, ad0 + off, bd0 + off, idesc_s, x > 0 || kk > 0 ? 1u : 0u);
                     }
+                    commit(issue, &kv_empty[stage]);
                 }
-                if (lane == 0) {
-                    mma_commit(smem_u32(&s_full[buf]));
-                    if (j == n - 1) mma_commit(smem_u32(q_empty));
-                }
-                __syncwarp();
+                commit(issue, &s_full[buf]);
+                if (j == n - 1) commit(issue, q_empty);
                 return true;
             };
             ok = issue_s(0) && (n < 2 || issue_s(1));
             for (int j = 0; ok && j < n; ++j) {
                 const int t = jj + j, buf = t & 1, og = NG == 2 ? buf : 0;
-                const uint32_t row = pv.row(c, h);
+                const uint32_t have = __ballot_sync(0xffffffffu, pv.valid(c));
                 if (j + 1 < n) pv.ahead(c, s.b, key0 + (j + 1) * kBlkKeys + lane * br, s.hi, nbox, lane);
-                const uint32_t have = __ballot_sync(0xffffffffu, row != kNoRow);
                 const int live = s.hi - (key0 + j * kBlkKeys);  // rows of the tile before the end
                 if (!__all_sync(0xffffffffu, mbar_wait(&p_full[buf], (t >> 1) & 1, err, ERR_BLOCK_MMA))) {
                     ok = false;
@@ -301,7 +435,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t tp = t_s + buf * kBlkKeys, t_o = tmem + og * HD;
+                const uint32_t tp = t_s + buf * kBlkKeys + 64, t_o = tmem + og * HD;
                 const bool first = j < NG;  // nothing in this O yet
 #pragma unroll
                 for (int x = 0; x < L::NS; ++x) {
@@ -322,44 +456,49 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                     }
-                    if (lane == 0) {
+                    const uint64_t vd0 = sdesc_sw128_mn(sv, kBlkKeys * 128);
 #pragma unroll
-                        for (int kk = 0; kk < kBlkKeys / 16; ++kk) {
-                            const uint64_t vd = sdesc_sw128_mn(sv + kk * 2048, kBlkKeys * 128);
-                            mma_ts(t_o + x * L::SC, tp + kk * 8, vd, idesc_pv, !first || kk > 0 ? 1u : 0u);
-                        }
-                        mma_commit(smem_u32(&kv_empty[stage]));
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < kBlkKeys / 16; ++kk)
+                        mma_ts(issue, t_o + x * L::SC, tp + kk * 8, vd0 + kk * (2048 / 16), idesc_pv,
+                               !first || kk > 0 ? 1u : 0u);
+                    commit(issue, &kv_empty[stage]);
                 }
                 if (!ok) break;
-                if (lane == 0) mma_commit(smem_u32(&pv_done[buf]));
-                __syncwarp();
+                commit(issue, &pv_done[buf]);
                 if (j + 2 < n) ok = issue_s(j + 2);
             }
             jj += n;
             ++unit_no;
         }
-        if (lane == 0) {
-            mma_commit(smem_u32(drain));  // arrives when every MMA issued above has completed
-            mbar_wait(drain, 0, err, ERR_BLOCK_DRAIN);
-        }
+        commit(issue, drain);  // arrives when every MMA issued above has completed
+        mbar_wait(drain, 0, err, ERR_BLOCK_DRAIN);
         __syncwarp();
-    } else {
-        const int grp = NG == 2 ? (warp - 2) >> 2 : 0;
+    } else if (warp >= 4) {
+        const int grp = NG == 2 ? (warp - 4) >> 2 : 0;
         const int quarter = warp & 3;  // TMEM lanes this warp may access
         const int row = quarter * 32 + lane;
-        const int tid = threadIdx.x - 64;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t t_o = tmem + (NG == 2 ? grp * HD : 0) + lane_off;
-        const float fac = a.cap > 0.f ? a.scale * (2.f * kLog2e / a.cap) : a.scale * kLog2e;
+        constexpr int C = NG == 2 ? 32 : 64;  // score columns in registers (168 or 255 a thread)
+        const float fac = a.scale * kLog2e, inv_cap = a.cap > 0.f ? kLn2 / a.cap : 0.f;
         const uint32_t all_parts = (1u << nbox) - 1u;
+        // tanh's coefficients for raw scores: c_i (fac inv_cap)^(2i)
+        float tc[5];
+        {
+            const float w = fac * inv_cap, w2 = w * w;
+            float f = w2;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                tc[i] = kTanhCoef[i] * f;
+                f *= w2;
+            }
+        }
         int jj = 0;
-        bool ok = true;  // false after a wait ran out: the warp then only keeps the named barriers company
-        while (walk.next(c, a.p, lane, s, unit, b0, b1, u0)) {
-            const int h = unit / s.tiles, rt = unit % s.tiles, n = b1 - b0;
-            const int row0 = rt * a.p.R, rows = min(a.p.R, s.n * a.p.G - row0);
-            const int key0 = s.lo + b0 * kBlkKeys;
+        int unit_no = 0;
+        bool ok = true;
+        while (ok && next_piece()) {
+            const int h = s.h, n = s.n, row0 = s.row0, rows = s.rows, key0 = s.key0;
+            if (rows <= 0) continue;
             int vlo, vhi;
             visible(s.pos0 + (row0 + min(row, rows - 1)) / a.p.G, s.len, a.p.causal, a.p.window, vlo, vhi);
             // keys every row of this warp sees (ranges only move up with the row)
@@ -371,7 +510,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             pk.ahead(c, s.b, key0 + j * kBlkKeys + lane * br, s.hi, nbox, lane);
             for (; ok && j < n; j += NG) {
                 const int t = jj + j, buf = t & 1, k0 = key0 + j * kBlkKeys;
-                const uint32_t have = __ballot_sync(0xffffffffu, pk.row(c, h) != kNoRow);
+                const uint32_t have = __ballot_sync(0xffffffffu, pk.valid(c));
                 if (j + NG < n) pk.ahead(c, s.b, k0 + NG * kBlkKeys + lane * br, s.hi, nbox, lane);
                 const uint32_t tb = t_s + buf * kBlkKeys + lane_off;
                 if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (t >> 1) & 1, err, ERR_BLOCK_SOFTMAX))) {
@@ -379,38 +518,35 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                float x[kBlkKeys];
+                // maximum of the raw scores (scale > 0 and the cap keep their order), C columns at a
+                // time; the last C stay in registers
+                const bool cut = have != all_parts || k0 < all_lo || k0 + kBlkKeys > all_hi;
+                float x[C];
+                float mx[4], mn = INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(tb + 32 * q, reinterpret_cast<uint32_t(&)[32]>(x[32 * q]));
-                tmem_ld_wait();
-                if (a.cap > 0.f) {
+                for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kBlkKeys; c0 += C) {
+                    load_scores<C>(tb + c0, x);
+                    if constexpr (CAP) {
+                        float lo[4] = {mn, x[1], x[2], x[3]};
 #pragma unroll
-                    for (int e = 0; e < kBlkKeys; ++e) x[e] = capped_log2(x[e] * fac, a.cap);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kBlkKeys; ++e) x[e] *= fac;
-                }
-                if (have != all_parts || k0 < all_lo || k0 + kBlkKeys > all_hi) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t bits = range_bits(vlo, vhi, k0 + 32 * q);
-                        if (have != all_parts) {
-                            uint32_t parts = 0;
-                            for (int e = 0; e < 32; ++e) parts |= ((have >> ((32 * q + e) >> log2_br)) & 1u) << e;
-                            bits &= parts;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((bits >> e) & 1u)) x[32 * q + e] = -INFINITY;
+                        for (int e = 0; e < C; ++e) lo[e & 3] = fminf(lo[e & 3], x[e]);
+                        mn = fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3]));
                     }
+                    if (cut) mask_scores<C>(x, vlo, vhi, k0 + c0, c0, have, log2_br);
+#pragma unroll
+                    for (int e = 0; e < C; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
                 }
-                float mx[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mx[e] = x[e];
-#pragma unroll
-                for (int e = 8; e < kBlkKeys; ++e) mx[e & 7] = fmaxf(mx[e & 7], x[e]);
-                const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                       fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                bool small = false;
+                float mt = raw * fac;
+                if constexpr (CAP) {
+                    small = __all_sync(0xffffffffu, (raw == -INFINITY || fabsf(mt * inv_cap) <= kTanhSmall) &&
+                                                        fabsf(mn * fac * inv_cap) <= kTanhSmall);
+                    if (raw > -INFINITY)
+                        mt = small ? capped_small(mt, mt * inv_cap) : capped_any(mt * inv_cap, kLog2e * a.cap);
+                }
                 const bool move = mt > m_run + kRescale || (m_run == -INFINITY && mt > -INFINITY);
                 float corr = 1.f;
                 if (move) {
@@ -438,19 +574,57 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     }
                     tmem_st_wait();
                 }
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float p0 = ex2(x[64 * half + 2 * e] - mu), p1 = ex2(x[64 * half + 2 * e + 1] - mu);
-                        ls[e & 3] += p0 + p1;
-                        p[e] = H2::pack(p0, p1);
+                f32x2 ls[2] = {0ull, 0ull};
+                const f32x2 fac2 = pair(fac, fac), nmu2 = pair(-mu, -mu);
+#pragma unroll 1
+                for (int c0 = kBlkKeys - C; c0 >= 0; c0 -= C) {
+                    if (c0 < kBlkKeys - C) {
+                        load_scores<C>(tb + c0, x);
+                        if (cut) mask_scores<C>(x, vlo, vhi, k0 + c0, c0, have, log2_br);
                     }
-                    tmem_st32(tb + 32 * half, p);
+                    uint32_t p[C / 2];
+                    if constexpr (!CAP) {
+#pragma unroll
+                        for (int e = 0; e < C / 2; ++e) {
+                            const float2 y = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), fac2, nmu2));
+                            const float p0 = ex2(y.x), p1 = ex2(y.y);
+                            ls[e & 1] = add2(ls[e & 1], pair(p0, p1));
+                            p[e] = H2::pack(p0, p1);
+                        }
+                    } else if (small && !cut) {  // capped_small in pairs, its powers of 1 / cap in the coefficients
+#pragma unroll
+                        for (int e = 0; e < C / 2; ++e) {
+                            const f32x2 v = pair(x[2 * e], x[2 * e + 1]), z = mul2(v, v);
+                            f32x2 q = fma2(z, pair(tc[4], tc[4]), pair(tc[3], tc[3]));
+                            q = fma2(z, q, pair(tc[2], tc[2]));
+                            q = fma2(z, q, pair(tc[1], tc[1]));
+                            q = fma2(z, q, pair(tc[0], tc[0]));
+                            q = fma2(z, q, pair(1.f, 1.f));
+                            const float2 y = unpair(fma2(mul2(v, fac2), q, nmu2));
+                            const float p0 = ex2(y.x), p1 = ex2(y.y);
+                            ls[e & 1] = add2(ls[e & 1], pair(p0, p1));
+                            p[e] = H2::pack(p0, p1);
+                        }
+                    } else {
+                        const float cap2 = kLog2e * a.cap;
+#pragma unroll
+                        for (int e = 0; e < C / 2; ++e) {
+                            float pe[2];
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                const float v = x[2 * e + w];
+                                pe[w] = v == -INFINITY ? 0.f : ex2(capped_any(v * fac * inv_cap, cap2) - mu);
+                            }
+                            ls[e & 1] = add2(ls[e & 1], pair(pe[0], pe[1]));
+                            p[e] = H2::pack(pe[0], pe[1]);
+                        }
+                    }
+                    // P of columns c0 .. over columns 64 + c0 / 2 .. of S_j, whose scores have been read by now
+#pragma unroll
+                    for (int e = 0; e < C / 2; e += 16) tmem_st16(tb + 64 + c0 / 2 + e, p + e);
                 }
-                l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                const float2 lsum = unpair(add2(ls[0], ls[1]));
+                l_run += lsum.x + lsum.y;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -461,29 +635,35 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 const int tp = jj + n - e;
                 ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[tp & 1], (tp >> 1) & 1, err, ERR_BLOCK_SOFTMAX));
             }
+            if (!ok) break;
             tc_fence_after();
             jj += n;
             float f0 = 1.f, f1 = 0.f, m = m_run, l = l_run;
-            bool has0 = true, has1 = false;
+            bool has0 = n > 0, has1 = false;
             if constexpr (NG == 2) {
-                s_ml[grp * kBlkRows + row] = make_float2(m_run, l_run);
-                bar_sync(1, NG * 128);
-                const float2 A = s_ml[row], B = s_ml[kBlkRows + row];
+                // (two sets of s_ml in turn: who writes the next but one has seen all arrive at the next)
+                float2* ml = s_ml + (unit_no & 1) * (NG * kBlkRows);
+                ml[grp * kBlkRows + row] = make_float2(m_run, l_run);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+                if (!__all_sync(0xffffffffu, mbar_wait(ml_full, unit_no & 1, err, ERR_BLOCK_SOFTMAX))) break;
+                ++unit_no;
+                const float2 A = ml[row], B = ml[kBlkRows + row];
                 const int j_first = (jj - n) & 1;  // the group of the unit's first tile
-                has0 = n > 1 || j_first == 0;
-                has1 = n > 1 || j_first == 1;
+                has0 = n > 1 || (n == 1 && j_first == 0);
+                has1 = n > 1 || (n == 1 && j_first == 1);
                 m = fmaxf(A.x, B.x);
                 f0 = A.x == -INFINITY ? 1.f : ex2(A.x - m);
                 f1 = B.x == -INFINITY ? 1.f : ex2(B.x - m);
                 l = A.y * f0 + B.y * f1;
             }
-            const bool whole = b0 == 0 && b1 == s.blocks, live = ok && row < rows;
-            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (b0 == 0 ? 1 : 0);
-            const Tile tile{s.first, row0, rows, h};
+            const bool whole = s.whole, live = row < rows;
+            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.starts ? 1 : 0);
             const int c_begin = NG == 2 ? grp * (HD / 2) : 0, c_end = c_begin + HD / NG;
             const uint32_t to = tmem + lane_off;
 #pragma unroll 1
             for (int col = c_begin; col < c_end; col += 32) {
+                if (n == 0 && !whole && col > 0) break;  // nothing seen: (-inf, 0) alone
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = 0.f;
@@ -503,7 +683,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 if (!live) continue;
                 if (whole) {
                     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-                    const int tok = tile.first + (row0 + row) / a.p.G, head = h * a.p.G + (row0 + row) % a.p.G;
+                    const int tok = s.first + (row0 + row) / a.p.G, head = h * a.p.G + (row0 + row) % a.p.G;
                     uint4* dst = reinterpret_cast<uint4*>(a.out.p + (tok * a.out.ts + head * a.out.hs + col) * 2);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -515,31 +695,16 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                         a.lse[static_cast<size_t>(tok) * a.Hq + head] =
                             l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(part_o(a, HD, slot, row) + col);
+                    float4* dst = block_part(a, HD, slot, col, row);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        __stcg(dst + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
-                    if (col == 0) __stcg(reinterpret_cast<float2*>(part_ml(a, HD, slot, row)), make_float2(m, l));
+                    for (int e = 0; n > 0 && e < 8; ++e)
+                        __stcg(dst + e * kBlkRows, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+                    if (col == 0) __stcg(block_part_ml(a, HD, slot, row), make_float2(m, l));
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
-            if (!whole) {
-                const int c_first = static_cast<int>(u0 / walk.per);
-                const int c_last = static_cast<int>((u0 + s.blocks - 1) / walk.per);
-                __threadfence();
-                bar_sync(1, NG * 128);
-                if (tid == 0)
-                    *s_flag = ok && atomicInc(a.counters + c_first, c_last - c_first) ==
-                              static_cast<unsigned>(c_last - c_first);
-                bar_sync(1, NG * 128);
-                if (*s_flag) {  // every piece of this unit is in memory; the counter is back at zero
-                    __threadfence();
-                    join_pieces<HD>(a, tile, BF, 1.f, c_first, c_last, tid, NG * 128);
-                }
-            }
-            if (NG == 2 || !whole) bar_sync(1, NG * 128);  // s_ml and s_flag are free again
+            if (lane == 0 && n > 0) mbar_arrive(o_free);
         }
     }
     tc_fence_before();
@@ -548,6 +713,46 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Joins the units that paged_block_kernel's CTAs cut: block (c, y) adds 16 columns
+// of CTA c's row tile of the unit that starts in its team and goes on behind it, if
+// there is one (a.joins, written by the scheduler).  A launch of its own, because a
+// row tile's pieces are up to 128 KB each: the CTA that finishes last would read
+// them alone (80 us for one canvas of 256 tokens at hd 256).
+constexpr int kJoinCols = 16;
+template <int HD, bool BF>
+__global__ void __launch_bounds__(256) paged_block_join_kernel(const AttendArgs a) {
+    using H2 = Half2<BF>;
+    pdl_enter();
+    const int cta = blockIdx.x, member = cta % a.p.TS;
+    const Piece s = a.joins[cta];
+    const int row = threadIdx.x & (kBlkRows - 1), col = blockIdx.y * kJoinCols + (threadIdx.x >> 7) * 8;
+    if (s.end || row >= s.rows) return;
+    float m = -INFINITY, l = 0.f, v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll 4
+    for (int k = s.t_first; k <= s.t_last; ++k) {  // in piece order
+        const size_t slot = 2 * static_cast<size_t>(k * a.p.TS + member) + (k == s.t_first ? 1 : 0);
+        const float2 ml = __ldcg(block_part_ml(a, HD, slot, row));
+        const float4 x0 = __ldcg(block_part(a, HD, slot, col, row)), x1 = __ldcg(block_part(a, HD, slot, col + 4, row));
+        const float mn = fmaxf(m, ml.x);
+        const float fo = m == -INFINITY ? 1.f : ex2(m - mn), fn = ml.x == -INFINITY ? 1.f : ex2(ml.x - mn);
+        const bool none = ml.x == -INFINITY && ml.y == 0.f;  // no key seen: nothing was written
+        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * fo + (none ? 0.f : x[e] * fn);
+        l = l * fo + ml.y * fn;
+        m = mn;
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int tok = s.first + (s.row0 + row) / a.p.G, head = s.h * a.p.G + (s.row0 + row) % a.p.G;
+    *reinterpret_cast<uint4*>(a.out.p + (tok * a.out.ts + head * a.out.hs + col) * 2) =
+        make_uint4(H2::pack(v[0] * inv, v[1] * inv), H2::pack(v[2] * inv, v[3] * inv),
+                   H2::pack(v[4] * inv, v[5] * inv), H2::pack(v[6] * inv, v[7] * inv));
+    if (a.lse != nullptr && col == 0)
+        a.lse[static_cast<size_t>(tok) * a.Hq + head] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace paged

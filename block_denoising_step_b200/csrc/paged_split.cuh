@@ -14,7 +14,7 @@
 // only one that shows.
 //
 // Memory-bound: every visible K and V row is read once.  Each warp streams its
-// own 16-key tiles through a private ring of shared memory (cp.async 16 bytes,
+// own tiles of 16 or 32 keys through a private ring of shared memory (cp.async 16 bytes,
 // XOR-swizzled by row; no block barrier in the loop); the page of each row is
 // looked up per key, one tile ahead, so a page may end anywhere in a tile.  Rows
 // outside the sequence's visible range or without a page are filled with zeros
@@ -33,20 +33,22 @@ namespace dgen {
 namespace paged {
 
 constexpr int kSplitWarps = 4;
-constexpr int kTileKeys = 16;                        // keys per warp tile
-constexpr int kBlockKeys = kSplitWarps * kTileKeys;  // keys per block of the line
 
-template <int HD, int ES>
+template <int HD, int ES, int NT>
 struct SplitLayout {
     static constexpr int ROWB = HD * ES;        // bytes of a cache row
     static constexpr int CH = ROWB / 16;        // 16-byte chunks of a row
-    static constexpr int TILE = kTileKeys * ROWB;
+    // 16-key steps per warp tile: 8 KB of K and V where registers allow
+    static constexpr int MT = NT == 1 && ROWB <= 128 ? 2 : 1;
+    static constexpr int KEYS = 16 * MT;                      // keys per warp tile
+    static constexpr int BLOCK_KEYS = kSplitWarps * KEYS;     // keys per block of the line
+    static constexpr int TILE = KEYS * ROWB;
     static constexpr int STAGES = 3;
     static constexpr int RING = kSplitWarps * STAGES * 2 * TILE;
 };
 template <int HD, int ES, int NT>
 struct SplitSmem {
-    using L = SplitLayout<HD, ES>;
+    using L = SplitLayout<HD, ES, NT>;
     static constexpr int R = 8 * NT;
     static constexpr int OP = HD + 4;  // padded row of the join buffers
     static constexpr int JOIN = kSplitWarps * R * OP * 4;
@@ -55,7 +57,9 @@ struct SplitSmem {
     static constexpr int ML_OFF = QS_OFF + R * 4;                 // float m[W][R], l[W][R]
     static constexpr int MASK_OFF = ML_OFF + 2 * kSplitWarps * R * 4;  // uint32 mask[W][STAGES]
     static constexpr int FLAG_OFF = MASK_OFF + kSplitWarps * L::STAGES * 4;
-    static constexpr int BYTES = (FLAG_OFF + 16 + 15) & ~15;
+    static constexpr int PIECE_OFF = FLAG_OFF + 16;                     // the current piece
+    static constexpr int WALK_OFF = PIECE_OFF + 64;                     // Walk[32]: warp 0's, a lane each
+    static constexpr int BYTES = (WALK_OFF + 32 * static_cast<int>(sizeof(Walk)) + 15) & ~15;
 };
 
 // chunk position of chunk c in row r: eight rows of one chunk column fall into
@@ -91,10 +95,11 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v) {
 // (else fp16; always fp16 for E4M3 caches).  NT: tiles of 8 query rows.
 template <int HD, int ES, bool BF, int NT>
 __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const AttendArgs a) {
-    using L = SplitLayout<HD, ES>;
+    using L = SplitLayout<HD, ES, NT>;
     using S = SplitSmem<HD, ES, NT>;
     using H2 = Half2<BF>;
-    constexpr int R = S::R, CH = L::CH, ST = L::STAGES, QCH = HD / 8;
+    constexpr int R = S::R, CH = L::CH, ST = L::STAGES, QCH = HD / 8, MT = L::MT, KEYS = L::KEYS;
+    constexpr uint32_t kAllKeys = KEYS == 32 ? 0xFFFFFFFFu : (1u << KEYS) - 1u;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t sbase = smem_u32(smem), ring = sbase + warp * (ST * 2 * L::TILE), sq = sbase + S::Q_OFF;
@@ -107,32 +112,43 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
 
     pdl_enter();
     const CacheView& c = a.c;
-    Walk walk;
-    walk.start(c, a.p, lane, a.min_blocks);
-    SeqInfo s;
-    int unit, b0, b1;
-    long long u0;
-    while (walk.next(c, a.p, lane, s, unit, b0, b1, u0)) {
-        const int h = unit / s.tiles, rt = unit % s.tiles;
-        const int row0 = rt * R, rows = min(R, s.n * a.p.G - row0);
-        // this tile's own key range within the sequence's
-        const int key_first = s.lo + b0 * kBlockKeys + warp * kTileKeys;
-        const int n_tiles = b1 - b0;
+    // warp 0 walks the units; its state waits in shared memory, not in the registers of the key loop
+    static_assert(sizeof(Piece) <= 64, "piece slot");
+    Piece& piece = *reinterpret_cast<Piece*>(smem + S::PIECE_OFF);
+    if (warp == 0) {
+        Walk walk;
+        walk.start(c, a.p, lane, a.min_blocks, blockIdx.x, a.n_ctas);
+        reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane] = walk;
+    }
+    for (;;) {
+        if (warp == 0) {
+            Walk walk = reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane];
+            Piece q{};
+            q.end = !walk.next(c, a.p, lane, q);
+            reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane] = walk;
+            if (lane == 0) piece = q;
+        }
+        __syncthreads();
+        const Piece s = piece;
+        if (s.end) break;
+        const int h = s.h, row0 = s.row0, rows = s.rows;
+        const int key_first = s.key0 + warp * KEYS;
+        const int n_tiles = s.n;
 
         // rows of the next tile to fetch: table entry loaded one tile ahead
-        int key_next = key_first + (lane & 15);
+        int key_next = key_first + (lane & (KEYS - 1));
         int id_next = key_next < s.hi ? page_entry(c, s.b, key_next / c.page) : -1;
         auto fetch = [&](int stage, bool live) {
             uint32_t row = kNoRow;
             if (live && key_next < s.hi) row = row_in_page(c, id_next, h, key_next % c.page);
-            key_next += kBlockKeys;
+            key_next += L::BLOCK_KEYS;
             id_next = live && key_next < s.hi ? page_entry(c, s.b, key_next / c.page) : -1;
-            const uint32_t mask = __ballot_sync(0xffffffffu, row != kNoRow) & 0xFFFFu;
+            const uint32_t mask = __ballot_sync(0xffffffffu, row != kNoRow) & kAllKeys;
             if (lane == 0) s_mask[stage] = mask;
             if (mask != 0) {
                 const uint32_t dk = ring + stage * (2 * L::TILE), dv = dk + L::TILE;
 #pragma unroll
-                for (int i = 0; i < kTileKeys * CH / 32; ++i) {
+                for (int i = 0; i < KEYS * CH / 32; ++i) {
                     const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
                     const uint32_t src = __shfl_sync(0xffffffffu, row, r);
                     const bool ok = src != kNoRow;
@@ -225,8 +241,9 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float f = a.scale * kscale * (ES == 1 ? qscale[nt * 8 + 2 * t4 + j] : 1.f);
-                fac[nt][j] = a.cap > 0.f ? f * (2.f * kLog2e / a.cap) : f * kLog2e;
+                fac[nt][j] = f * kLog2e;
             }
+        const float inv_cap = a.cap > 0.f ? kLn2 / a.cap : 0.f;  // of a log2-domain score
 
         float o[HD / 16][NT][4];
         float m_run[NT][2], l_run[NT][2];
@@ -245,71 +262,117 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
             __syncwarp();
             const int stage = i % ST;
             const uint32_t mask = s_mask[stage];
-            const int key0 = key_first + i * kBlockKeys;
+            const int key0 = key_first + i * L::BLOCK_KEYS;
             if (mask != 0) {  // (warp-uniform)
                 const uint32_t tk = ring + stage * (2 * L::TILE), tv = tk + L::TILE;
-                float sc[NT][4];
+                float sc[MT][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int km = 0; km < MT; ++km)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[km][nt][e] = 0.f;
                 // S^T = K Q^T, 32 elements of hd per step
 #pragma unroll
                 for (int kk = 0; kk < HD / 32; ++kk) {
-                    uint32_t ka[2][4];
-                    const int r = lane & 15;
-                    if constexpr (ES == 2) {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            attn::ldsm_x4(tk + r * L::ROWB + swz_chunk<CH>(r, 4 * kk + 2 * u + (lane >> 4)) * 16,
-                                          ka[u][0], ka[u][1], ka[u][2], ka[u][3]);
-                    } else {
-                        uint32_t x[4];  // keys 0-7 / 8-15 of the first 16 bytes, then of the second
-                        attn::ldsm_x4(tk + r * L::ROWB + swz_chunk<CH>(r, 2 * kk + (lane >> 4)) * 16, x[0], x[1],
-                                      x[2], x[3]);
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const uint32_t v = x[2 * u + half];
-                                ka[u][half] = e4m3x2_f16x2(static_cast<uint16_t>(v));
-                                ka[u][2 + half] = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
-                            }
-                    }
+                    uint32_t b[NT][4];  // k 0-7, 8-15, 16-23, 24-31 of query rows nt * 8 ..
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t b[4];  // k 0-7, 8-15, 16-23, 24-31 of rows nt * 8 ..
                         const int qr = nt * 8 + (lane & 7);
-                        attn::ldsm_x4(sq + qr * (HD * 2) + swz_chunk<QCH>(qr, 4 * kk + (lane >> 3)) * 16, b[0], b[1],
-                                      b[2], b[3]);
-                        mma_16816<BF>(sc[nt], ka[0], b[0], b[1]);
-                        mma_16816<BF>(sc[nt], ka[1], b[2], b[3]);
+                        attn::ldsm_x4(sq + qr * (HD * 2) + swz_chunk<QCH>(qr, 4 * kk + (lane >> 3)) * 16, b[nt][0],
+                                      b[nt][1], b[nt][2], b[nt][3]);
+                    }
+#pragma unroll
+                    for (int km = 0; km < MT; ++km) {
+                        uint32_t ka[2][4];
+                        const int r = km * 16 + (lane & 15);
+                        if constexpr (ES == 2) {
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                attn::ldsm_x4(tk + r * L::ROWB + swz_chunk<CH>(r, 4 * kk + 2 * u + (lane >> 4)) * 16,
+                                              ka[u][0], ka[u][1], ka[u][2], ka[u][3]);
+                        } else {
+                            uint32_t x[4];  // keys 0-7 / 8-15 of the first 16 bytes, then of the second
+                            attn::ldsm_x4(tk + r * L::ROWB + swz_chunk<CH>(r, 2 * kk + (lane >> 4)) * 16, x[0], x[1],
+                                          x[2], x[3]);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    const uint32_t v = x[2 * u + half];
+                                    ka[u][half] = e4m3x2_f16x2(static_cast<uint16_t>(v));
+                                    ka[u][2 + half] = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
+                                }
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_16816<BF>(sc[km][nt], ka[0], b[nt][0], b[nt][1]);
+                            mma_16816<BF>(sc[km][nt], ka[1], b[nt][2], b[nt][3]);
+                        }
                     }
                 }
                 // log2-domain scores, masks, running maximum
-                const bool full = mask == 0xFFFFu && key0 >= all_lo && key0 + kTileKeys <= all_hi;
+                if (a.cap > 0.f) {
+                    bool small = true;
+#pragma unroll
+                    for (int km = 0; km < MT; ++km)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                small &= fabsf(sc[km][nt][e] * fac[nt][e & 1] * inv_cap) <= kTanhSmall;
+                    if (__all_sync(0xffffffffu, small)) {
+#pragma unroll
+                        for (int km = 0; km < MT; ++km)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float x = sc[km][nt][e] * fac[nt][e & 1];
+                                    sc[km][nt][e] = capped_small(x, x * inv_cap);
+                                }
+                    } else {
+#pragma unroll
+                        for (int km = 0; km < MT; ++km)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    sc[km][nt][e] =
+                                        capped_any(sc[km][nt][e] * fac[nt][e & 1] * inv_cap, kLog2e * a.cap);
+                    }
+                } else {
+#pragma unroll
+                    for (int km = 0; km < MT; ++km)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sc[km][nt][e] *= fac[nt][e & 1];
+                }
+                if (!(mask == kAllKeys && key0 >= all_lo && key0 + KEYS <= all_hi)) {
+#pragma unroll
+                    for (int km = 0; km < MT; ++km)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int kr = km * 16 + g + 8 * (e >> 1), key = key0 + kr;
+                                if (!((mask >> kr) & 1u) || key < vlo[nt][e & 1] || key >= vhi[nt][e & 1])
+                                    sc[km][nt][e] = -INFINITY;
+                            }
+                }
                 bool move = false;
-                float mt_[NT][2];
+                float top[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float x0 = sc[nt][j] * fac[nt][j], x1 = sc[nt][2 + j] * fac[nt][j];
-                        if (a.cap > 0.f) {
-                            x0 = capped_log2(x0, a.cap);
-                            x1 = capped_log2(x1, a.cap);
-                        }
-                        if (!full) {
-                            const int k0 = key0 + g, k1 = k0 + 8;
-                            if (!((mask >> g) & 1u) || k0 < vlo[nt][j] || k0 >= vhi[nt][j]) x0 = -INFINITY;
-                            if (!((mask >> (g + 8)) & 1u) || k1 < vlo[nt][j] || k1 >= vhi[nt][j]) x1 = -INFINITY;
-                        }
-                        sc[nt][j] = x0;
-                        sc[nt][2 + j] = x1;
-                        float mx = fmaxf(x0, x1);
+                        float mx = fmaxf(sc[0][nt][j], sc[0][nt][2 + j]);
+#pragma unroll
+                        for (int km = 1; km < MT; ++km) mx = fmaxf(mx, fmaxf(sc[km][nt][j], sc[km][nt][2 + j]));
 #pragma unroll
                         for (int w = 4; w <= 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                        mt_[nt][j] = mx;
+                        top[nt][j] = mx;
                         move |= mx > m_run[nt][j] + kRescale || (m_run[nt][j] == -INFINITY && mx > -INFINITY);
                     }
                 if (__any_sync(0xffffffffu, move)) {
@@ -318,7 +381,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                         float corr[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const float mn = fmaxf(m_run[nt][j], mt_[nt][j]);
+                            const float mn = fmaxf(m_run[nt][j], top[nt][j]);
                             corr[j] = m_run[nt][j] == -INFINITY ? 0.f : exp2f(m_run[nt][j] - mn);
                             m_run[nt][j] = mn;
                             l_run[nt][j] *= corr[j];
@@ -329,59 +392,65 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                             for (int e = 0; e < 4; ++e) o[mt][nt][e] *= corr[e & 1];
                     }
                 }
-                uint32_t ph[NT][2], pl[NT][2];
+                uint32_t ph[MT][NT][2], pl[MT][NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
+                for (int km = 0; km < MT; ++km)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
-                        p[e] = exp2f(sc[nt][e] - mu);
-                        l_run[nt][e & 1] += p[e];
-                    }
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float p[4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t hi = H2::pack(p[2 * half], p[2 * half + 1]);
-                        const float2 hf = H2::unpack(hi);
-                        ph[nt][half] = movmatrix_t(hi);
-                        pl[nt][half] = movmatrix_t(H2::pack(p[2 * half] - hf.x, p[2 * half + 1] - hf.y));
-                    }
-                }
-                // O^T += V^T P^T
-                const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
-                if constexpr (ES == 2) {
+                        for (int e = 0; e < 4; ++e) {
+                            const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+                            p[e] = exp2f(sc[km][nt][e] - mu);
+                            l_run[nt][e & 1] += p[e];
+                        }
 #pragma unroll
-                    for (int mt = 0; mt < HD / 16; ++mt) {
-                        uint32_t va[4];
-                        attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mt + vc) * 16, va[0], va[1], va[2],
-                                        va[3]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_16816<BF>(o[mt][nt], va, ph[nt][0], ph[nt][1]);
-                            mma_16816<BF>(o[mt][nt], va, pl[nt][0], pl[nt][1]);
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t hi = H2::pack(p[2 * half], p[2 * half + 1]);
+                            const float2 hf = H2::unpack(hi);
+                            ph[km][nt][half] = movmatrix_t(hi);
+                            pl[km][nt][half] = movmatrix_t(H2::pack(p[2 * half] - hf.x, p[2 * half + 1] - hf.y));
                         }
                     }
-                } else {
+                // O^T += V^T P^T
+                const int vc = (lane >> 3) & 1;
 #pragma unroll
-                    for (int mp = 0; mp < HD / 32; ++mp) {
-                        uint32_t x[4];  // two 16-byte columns x keys 0-7, then keys 8-15
-                        attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mp + vc) * 16, x[0], x[1], x[2],
-                                        x[3]);
+                for (int km = 0; km < MT; ++km) {
+                    const int vr = km * 16 + (lane & 7) + ((lane >> 4) << 3);
+                    if constexpr (ES == 2) {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
+                        for (int mt = 0; mt < HD / 16; ++mt) {
                             uint32_t va[4];
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const uint32_t v = x[2 * half + u];
-                                const uint32_t e0 = e4m3x2_f16x2(static_cast<uint16_t>(v));
-                                const uint32_t e1 = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
-                                va[2 * half] = __byte_perm(e0, e1, 0x5410);      // byte 2g: row g
-                                va[2 * half + 1] = __byte_perm(e0, e1, 0x7632);  // byte 2g + 1: row g + 8
-                            }
+                            attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mt + vc) * 16, va[0], va[1],
+                                            va[2], va[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                mma_16816<BF>(o[2 * mp + u][nt], va, ph[nt][0], ph[nt][1]);
-                                mma_16816<BF>(o[2 * mp + u][nt], va, pl[nt][0], pl[nt][1]);
+                                mma_16816<BF>(o[mt][nt], va, ph[km][nt][0], ph[km][nt][1]);
+                                mma_16816<BF>(o[mt][nt], va, pl[km][nt][0], pl[km][nt][1]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int mp = 0; mp < HD / 32; ++mp) {
+                            uint32_t x[4];  // two 16-byte columns x keys 0-7, then keys 8-15
+                            attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mp + vc) * 16, x[0], x[1], x[2],
+                                            x[3]);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                uint32_t va[4];
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    const uint32_t v = x[2 * half + u];
+                                    const uint32_t e0 = e4m3x2_f16x2(static_cast<uint16_t>(v));
+                                    const uint32_t e1 = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
+                                    va[2 * half] = __byte_perm(e0, e1, 0x5410);      // byte 2g: row g
+                                    va[2 * half + 1] = __byte_perm(e0, e1, 0x7632);  // byte 2g + 1: row g + 8
+                                }
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma_16816<BF>(o[2 * mp + u][nt], va, ph[km][nt][0], ph[km][nt][1]);
+                                    mma_16816<BF>(o[2 * mp + u][nt], va, pl[km][nt][0], pl[km][nt][1]);
+                                }
                             }
                         }
                     }
@@ -423,9 +492,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                     }
             }
         __syncthreads();
-        const bool whole = b0 == 0 && b1 == s.blocks;
-        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (b0 == 0 ? 1 : 0);
-        const Tile tile{s.first, row0, rows, h};
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.starts ? 1 : 0);
         const bool out_bf = ES == 2 ? BF : a.q_bf16 != 0;
         const float vscale = ES == 1 ? __ldg(c.v_scale + h) : 1.f;
         for (int i = threadIdx.x; i < rows * (HD / 4); i += kSplitWarps * 32) {
@@ -440,24 +507,22 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                 // (a warp without a maximum has l = 0, or NaN from NaN scores)
                 l += s_l[w * R + r] * (s_m[w * R + r] == -INFINITY ? 1.f : exp2f(s_m[w * R + r] - m));
             }
-            if (whole) {
-                store4(a, tile, out_bf, vscale, r, col, v, m, l);
+            if (s.whole) {
+                store4(a, s, out_bf, vscale, r, col, v, m, l);
             } else {
                 __stcg(reinterpret_cast<float4*>(part_o(a, HD, slot, r) + col), v);
                 if (col == 0) __stcg(reinterpret_cast<float2*>(part_ml(a, HD, slot, r)), make_float2(m, l));
             }
         }
-        if (!whole) {
-            const int c_first = static_cast<int>(u0 / walk.per);
-            const int c_last = static_cast<int>((u0 + s.blocks - 1) / walk.per);
+        if (!s.whole) {
+            const unsigned last = s.t_last - s.t_first;
             __threadfence();
             __syncthreads();
-            if (threadIdx.x == 0)
-                *s_flag = atomicInc(a.counters + c_first, c_last - c_first) == static_cast<unsigned>(c_last - c_first);
+            if (threadIdx.x == 0) *s_flag = atomicInc(a.counters + s.t_first, last) == last;
             __syncthreads();
             if (*s_flag) {  // every piece of this unit is in memory; the counter is back at zero
                 __threadfence();
-                join_pieces<HD>(a, tile, out_bf, vscale, c_first, c_last, threadIdx.x, kSplitWarps * 32);
+                join_pieces<HD>(a, s, 0, out_bf, vscale, 0, rows, threadIdx.x, kSplitWarps * 32);
             }
         }
         __syncthreads();  // join buffers free before the next unit's copies

@@ -1,13 +1,18 @@
 // How the attention kernels over the paged cache divide a batch of unequal
 // sequences, without the host knowing their lengths.
 //
-// A unit is one row tile (up to R of the n_b * G query rows that share a KV
-// head) of one sequence and KV head; its keys are dealt in blocks of KB.  All
-// units' blocks, in unit order, form one line of T blocks, which is cut into
-// equal pieces, one per CTA: each CTA finds T and its first unit by scanning the
-// lengths (32 sequences per step).  A unit cut by a piece's end is finished by
-// the CTA that completes last, from the partial results (O, m, l) of all pieces,
-// added in piece order: which CTA does it does not change the result.
+// The n_b * G query rows that share a KV head of a sequence are cut into row tiles
+// of R; TS neighbouring row tiles form a unit (sequence, KV head, super tile), whose
+// keys are dealt in blocks of KB.  All units' blocks, in unit order, form one line
+// of T blocks, cut into equal pieces, one per team of TS CTAs; member m of a team
+// computes row tile m of each unit, so that the team reads the same keys at the same
+// time and all but one member find them in L2 (separate units per CTA read them from
+// HBM once per row tile: 1.2 GB instead of 0.3 for eight canvases over 4096 tokens).
+// A unit counts the blocks its own rows see (causal order, window), so a prompt's
+// first rows weigh little.  Each warp finds T and its piece by scanning the lengths,
+// 32 sequences per step; the prefix sums over a sequence's units have a closed form.
+// A unit cut by a piece's end is joined from its pieces' partial results (O, m, l),
+// added in piece order: which CTA or thread does it does not change the result.
 #pragma once
 
 #include "paged.cuh"
@@ -23,33 +28,77 @@ struct SeqInfo {
     int first, n;      // token rows
     int len;           // keys (kv_len, at most what the table can hold)
     int pos0;          // position of the first new token
-    int lo, hi;        // keys any of its queries sees
-    int tiles;         // row tiles
-    int blocks;        // key blocks per unit
+    int tiles;         // super tiles
+    int lo, blocks;    // irregular: first key and blocks of every unit
+    int regular;       // units have ranges of their own (prefix_blocks)
     int b;
-    long long end;     // T of all sequences up to and including this one
+    int head;          // blocks of all super tiles of one KV head
+    int end;           // blocks of all sequences up to and including this one (the host keeps T below 2^31)
 };
 
 struct Partition {
-    int G, R, KB, align, causal, window;  // align: blocks start at multiples of it (a power of two)
+    int G, R, TS, KB, causal, window;
+    int align;               // blocks start at multiples of it: KB, or 1 where sequences have one tile
     int rows_min, rows_max;  // query rows per KV head of the sequences this launch takes
 };
 
-__device__ __forceinline__ long long warp_inclusive(long long v, int lane) {
+// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid's scheme on the lattice
+// points below the line)
+__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long sum = 0;
+    while (n > 0) {
+        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+// Blocks of the super tiles before number k of a regular sequence (pos0 >= 0,
+// len = pos0 + n): tile i holds the tokens i T .. (T = tokens of a super tile) and
+// sees blocks floor(lo / KB) .. ceil(hi / KB) - 1.
+__host__ __device__ inline long long prefix_blocks(const SeqInfo& s, const Partition& p, int k) {
+    const long long T = p.R / p.G * p.TS, KB = p.KB, n = s.n, w = p.window, whole = (s.len + KB - 1) / KB;
+    long long up;  // sum of ceil(hi / KB)
+    if (p.causal) {
+        const long long m = k < s.tiles ? k : s.tiles - 1;  // the last tile may be short
+        up = floor_sum(m, KB, T, s.pos0 + T + KB - 1) + (k - m) * whole;
+    } else if (w == 0) {
+        up = k * whole;
+    } else {  // hi = min(len, pos0 + (i + 1) T - 1 + w): reaches len from tile r on
+        long long r = n + 1 - w <= 0 ? 0 : (n + 1 - w + T - 1) / T - 1;
+        if (r < 0) r = 0;
+        if (r > s.tiles - 1) r = s.tiles - 1;
+        const long long m = k < r ? k : r;
+        up = floor_sum(m, KB, T, s.pos0 + T - 1 + w + KB - 1) + (k - m) * whole;
+    }
+    if (w == 0) return up;
+    // lo = max(0, pos0 + i T - w + 1): positive from tile r on
+    const long long d = w - 1 - s.pos0;
+    const long long r = d <= 0 ? 0 : (d + T - 1) / T;
+    return up - (k > r ? floor_sum(k - r, KB, T, s.pos0 + r * T - w + 1) : 0);
+}
+
+__device__ __forceinline__ int warp_inclusive(int v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
     return v;
 }
 
 // Lane's sequence of the 32 starting at base; .end = `before` + inclusive prefix.
-__device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partition& p, int base, long long before,
-                                              int lane) {
+__device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partition& p, int base, int before, int lane) {
     SeqInfo s{};
     s.b = base + lane;
-    long long w = 0;
     if (s.b < c.B) {
         seq_tokens(c, s.b, s.first, s.n);
         const int full = max(__ldg(c.kv_len + s.b), 0);
@@ -58,17 +107,17 @@ __device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partitio
         s.len = full < cap ? full : static_cast<int>(cap);
         const int rows = s.n * p.G;
         if (rows >= p.rows_min && rows <= p.rows_max && rows > 0) {
-            int lo1, hi0;
-            visible(s.pos0, s.len, p.causal, p.window, s.lo, hi0);
-            visible(s.pos0 + s.n - 1, s.len, p.causal, p.window, lo1, s.hi);
+            s.tiles = (rows + p.R * p.TS - 1) / (p.R * p.TS);
+            s.regular = s.tiles > 1 && p.align == p.KB && s.pos0 >= 0 && s.len == full;
+            int hi, x;
+            visible(s.pos0, s.len, p.causal, p.window, s.lo, x);
+            visible(s.pos0 + s.n - 1, s.len, p.causal, p.window, x, hi);
             s.lo &= ~(p.align - 1);
-            s.hi = max(s.hi, s.lo);
-            s.tiles = (rows + p.R - 1) / p.R;
-            s.blocks = max(1, (s.hi - s.lo + p.KB - 1) / p.KB);  // no key: one block that writes zeros
-            w = static_cast<long long>(s.tiles) * c.Hkv * s.blocks;
+            s.blocks = max(1, (hi - s.lo + p.KB - 1) / p.KB);  // no key: one block that writes zeros
+            s.head = s.regular ? static_cast<int>(prefix_blocks(s, p, s.tiles)) : s.tiles * s.blocks;
         }
     }
-    s.end = before + warp_inclusive(w, lane);
+    s.end = before + warp_inclusive(s.head * c.Hkv, lane);
     return s;
 }
 
@@ -79,62 +128,127 @@ __device__ __forceinline__ SeqInfo pick(const SeqInfo& s, int src) {
     r.n = __shfl_sync(f, s.n, src);
     r.len = __shfl_sync(f, s.len, src);
     r.pos0 = __shfl_sync(f, s.pos0, src);
-    r.lo = __shfl_sync(f, s.lo, src);
-    r.hi = __shfl_sync(f, s.hi, src);
     r.tiles = __shfl_sync(f, s.tiles, src);
+    r.lo = __shfl_sync(f, s.lo, src);
     r.blocks = __shfl_sync(f, s.blocks, src);
+    r.regular = __shfl_sync(f, s.regular, src);
     r.b = __shfl_sync(f, s.b, src);
+    r.head = __shfl_sync(f, s.head, src);
     r.end = __shfl_sync(f, s.end, src);
     return r;
 }
 
-// A warp's walk over the units of its CTA's piece.
-struct Walk {
-    SeqInfo mine;            // this lane's sequence of the current chunk
-    int base;                // first sequence of the chunk
-    long long total, per, t, t_end;
+// A piece of a unit, as one member of the team sees it.
+struct Piece {
+    int end;             // no piece: the walk is over
+    int b, h;            // sequence, KV head
+    int first, row0;     // first token row of the sequence, first query row of the row tile
+    int rows;            // its rows (<= 0: this member has none)
+    int pos0, len;
+    int key0;            // first key of this member's first block
+    int n;               // its blocks (0: it sees no key here)
+    int hi;              // keys from here on are not seen by any of its rows
+    int whole, starts;   // the piece is the whole unit / holds the unit's first block
+    int t_first, t_last; // teams that hold the unit's pieces
+};
 
-    __device__ __forceinline__ void start(const CacheView& c, const Partition& p, int lane, int min_blocks) {
-        long long before = 0;
+// A warp's walk over the units of its team's piece of the line.
+struct Walk {
+    SeqInfo mine;  // this lane's sequence of the current chunk
+    int base;      // first sequence of the chunk
+    int member;
+    int total, per, t, t_end;
+
+    __device__ __forceinline__ void start(const CacheView& c, const Partition& p, int lane, int min_blocks, int cta,
+                                          int n_ctas) {
+        int before = 0;
         for (base = 0;; base += 32) {
             mine = load_chunk(c, p, base, before, lane);
             before = __shfl_sync(0xffffffffu, mine.end, 31);
             if (base + 32 >= c.B) break;
         }
+        const int teams = n_ctas / p.TS;
+        member = cta % p.TS;
         total = before;
-        per = (total + gridDim.x - 1) / gridDim.x;
+        per = (total + teams - 1) / teams;
         if (per < min_blocks) per = min_blocks;
-        t = per * blockIdx.x;
-        t_end = t + per < total ? t + per : total;
+        // (per * team can pass 2^31 only behind the line's end)
+        const long long at = static_cast<long long>(per) * (cta / p.TS);
+        t = at < total ? static_cast<int>(at) : total;
+        t_end = per < total - t ? t + per : total;
         if (base > 0) {
             base = 0;
             mine = load_chunk(c, p, 0, 0, lane);
         }
     }
-    // The unit at t: its sequence, unit number within the sequence and blocks
-    // [b0, b1); false when the piece is done.  u0 is the unit's first block on
-    // the line.
-    __device__ __forceinline__ bool next(const CacheView& c, const Partition& p, int lane, SeqInfo& s, int& unit,
-                                         int& b0, int& b1, long long& u0) {
+    // The unit at t and this team's blocks of it; false when the piece is done.
+    __device__ __forceinline__ bool next(const CacheView& c, const Partition& p, int lane, Piece& q) {
         if (t >= t_end) return false;
-        long long chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
+        int chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
         while (t >= chunk_end) {
             base += 32;
             mine = load_chunk(c, p, base, chunk_end, lane);
             chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
         }
         const int src = __ffs(__ballot_sync(0xffffffffu, t < mine.end)) - 1;
-        s = pick(mine, src);
-        const long long seq0 = s.end - static_cast<long long>(s.tiles) * c.Hkv * s.blocks;
-        unit = static_cast<int>((t - seq0) / s.blocks);
-        u0 = seq0 + static_cast<long long>(unit) * s.blocks;
-        b0 = static_cast<int>(t - u0);
-        const long long left = t_end - u0;
-        b1 = left < s.blocks ? static_cast<int>(left) : s.blocks;
+        const SeqInfo s = pick(mine, src);
+        const int seq0 = s.end - s.head * c.Hkv;
+        q.h = (t - seq0) / s.head;
+        const int head0 = seq0 + q.h * s.head, x = t - head0;
+        // the super tile: the last k with prefix(k) <= x
+        int k, u0, blocks, lo;
+        if (!s.regular) {
+            k = x / s.blocks;
+            u0 = head0 + k * s.blocks;
+            blocks = s.blocks;
+            lo = s.lo;
+        } else {
+            int from = 0, to = s.tiles;  // prefix(from) <= x < prefix(to)
+            while (to - from > 1) {
+                const int step = (to - from + 31) / 32, at = from + lane * step;
+                const bool le = at < to && prefix_blocks(s, p, at) <= x;
+                const int cnt = __popc(__ballot_sync(0xffffffffu, le));
+                from += (cnt - 1) * step;
+                to = min(to, from + step);
+            }
+            k = from;
+            const int before = static_cast<int>(prefix_blocks(s, p, k));
+            u0 = head0 + before;
+            blocks = static_cast<int>(prefix_blocks(s, p, k + 1) - before);
+            const int p0 = s.pos0 + k * (p.R / p.G * p.TS);
+            lo = p.window > 0 && p0 >= p.window ? (p0 - p.window + 1) & ~(p.KB - 1) : 0;
+        }
+        const int b0 = t - u0, b1 = min(t_end - u0, blocks);
         t = u0 + b1;
+        q.end = 0;
+        q.b = s.b;
+        q.first = s.first;
+        q.pos0 = s.pos0;
+        q.len = s.len;
+        q.row0 = (k * p.TS + member) * p.R;
+        q.rows = min(p.R, s.n * p.G - q.row0);
+        q.whole = b0 == 0 && b1 == blocks;
+        q.starts = b0 == 0;
+        q.t_first = u0 / per;
+        q.t_last = (u0 + blocks - 1) / per;
+        q.n = 0;
+        q.hi = 0;
+        q.key0 = lo;
+        if (q.rows > 0) {  // this member's own range, in the unit's blocks
+            int my_lo, x0;
+            visible(s.pos0 + q.row0 / p.G, s.len, p.causal, p.window, my_lo, x0);
+            visible(s.pos0 + (q.row0 + q.rows - 1) / p.G, s.len, p.causal, p.window, x0, q.hi);
+            if (q.hi > my_lo) {
+                const int j0 = max(b0, (my_lo - lo) / p.KB), j1 = min(b1, (q.hi - lo + p.KB - 1) / p.KB);
+                q.n = max(0, j1 - j0);
+                q.key0 = lo + j0 * p.KB;
+            }
+        }
         return true;
     }
 };
+
+struct Piece;
 
 struct AttendArgs {
     CacheView c;
@@ -145,23 +259,33 @@ struct AttendArgs {
     float scale, cap;
     int q_bf16;
     unsigned int* counters;  // [grid]
-    float* parts;            // [2 grid][R][HD] then [2 grid][R][2]
-    int min_blocks;
+    Piece* joins;            // [grid], block kernel
+    float* parts;            // [2 n_ctas][R][HD] then [2 n_ctas][R][2]
+    int min_blocks, n_ctas;
 };
 
-// log2(e) cap tanh(s / cap) from x = 2 log2(e) s / cap, with tanh y = 1 - 2 / (1 + e^2y)
-__device__ __forceinline__ float capped_log2(float x, float cap) {
-    return kLog2e * cap * (1.f - __fdividef(2.f, 1.f + exp2f(x)));
+// Capped scores, log2(e) cap tanh(s / cap), from x = log2(e) s and u = s / cap.
+// tanh u = u (1 + z P(z)), z = u^2, for |u| <= 3/4 (a Chebyshev fit of tanh(u) / u in
+// z over that range, 9e-8 off in fp32): scores are mostly far below the cap, and
+// this needs no exponential or division, whose unit the softmax already fills.
+constexpr float kTanhSmall = 0.75f;
+__device__ constexpr float kTanhCoef[5] = {-0.3333296775817871f, 0.13325515389442444f, -0.053349819034338f,
+                                           0.01959378644824028f, -0.004723952151834965f};
+__device__ __forceinline__ float capped_small(float x, float u) {
+    const float z = u * u;
+    float p = kTanhCoef[4];
+#pragma unroll
+    for (int i = 3; i >= 0; --i) p = fmaf(p, z, kTanhCoef[i]);
+    return fmaf(x * z, p, x);
 }
-
-// One row tile: where its rows' outputs go.
-struct Tile {
-    int first, row0, rows, h;  // first token of the sequence, first and number of query rows, KV head
-};
+// any u: tanh u = 1 - 2 / (1 + e^2u); cap2 = log2(e) cap
+__device__ __forceinline__ float capped_any(float u, float cap2) {
+    return cap2 * (1.f - __fdividef(2.f, 1.f + exp2f(u * (2.f * kLog2e))));
+}
 
 // Four columns of a row: v / l (times the values' scale) rounded to the output
 // type; the row's log-sum-exp goes with column 0.  l = 0: no key seen.
-__device__ __forceinline__ void store4(const AttendArgs& a, const Tile& t, bool bf, float vscale, int r, int col,
+__device__ __forceinline__ void store4(const AttendArgs& a, const Piece& t, bool bf, float vscale, int r, int col,
                                        float4 v, float m, float l) {
     const int tok = t.first + (t.row0 + r) / a.p.G, head = t.h * a.p.G + (t.row0 + r) % a.p.G;
     const float inv = l > 0.f || l != l ? vscale / l : 0.f;
@@ -176,30 +300,32 @@ __device__ __forceinline__ void store4(const AttendArgs& a, const Tile& t, bool 
 }
 
 // Partial results: slot 2 c + 1 holds the piece that starts a unit in CTA c,
-// slot 2 c the one that continues it there.  O is relative to 2^m, not divided by l.
+// slot 2 c the one that continues it there.  O is relative to 2^m, not divided by l;
+// a piece that saw no key has m = -inf, l = 0 and no O.
 __device__ __forceinline__ float* part_o(const AttendArgs& a, int hd, size_t slot, int r) {
     return a.parts + (slot * a.p.R + r) * hd;
 }
 __device__ __forceinline__ float* part_ml(const AttendArgs& a, int hd, size_t slot, int r) {
-    return a.parts + 2 * static_cast<size_t>(gridDim.x) * a.p.R * hd + (slot * a.p.R + r) * 2;
+    return a.parts + 2 * static_cast<size_t>(a.n_ctas) * a.p.R * hd + (slot * a.p.R + r) * 2;
 }
 
-// Adds the pieces of a unit cut over CTAs c_first .. c_last, in that order, by
-// `threads` threads; all of them are in memory.
+// Adds the pieces of rows [r_begin, r_end) of a unit cut over teams t_first ..
+// t_last, in that order, by `threads` threads; all pieces are in memory.
 template <int HD>
-__device__ __forceinline__ void join_pieces(const AttendArgs& a, const Tile& t, bool bf, float vscale, int c_first,
-                                            int c_last, int tid, int threads) {
-    for (int i = tid; i < t.rows * (HD / 4); i += threads) {
+__device__ __forceinline__ void join_pieces(const AttendArgs& a, const Piece& t, int member, bool bf, float vscale,
+                                            int r_begin, int r_end, int tid, int threads) {
+    for (int i = r_begin * (HD / 4) + tid; i < r_end * (HD / 4); i += threads) {
         const int r = i / (HD / 4), col = (i % (HD / 4)) * 4;
         float m = -INFINITY, l = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int k = c_first; k <= c_last; ++k) {
-            const size_t slot = 2 * static_cast<size_t>(k) + (k == c_first ? 1 : 0);
+        for (int k = t.t_first; k <= t.t_last; ++k) {
+            const size_t slot = 2 * static_cast<size_t>(k * a.p.TS + member) + (k == t.t_first ? 1 : 0);
             const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml(a, HD, slot, r)));
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(part_o(a, HD, slot, r) + col));
+            float4 x = __ldcg(reinterpret_cast<const float4*>(part_o(a, HD, slot, r) + col));
+            if (ml.x == -INFINITY && ml.y == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
             const float mn = fmaxf(m, ml.x);
-            // (a piece without a maximum holds zeros, or NaN from NaN scores alone)
+            // (a piece without a maximum holds nothing, or NaN from NaN scores alone)
             const float fo = m == -INFINITY ? 1.f : exp2f(m - mn), fn = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mn);
             v.x = v.x * fo + x.x * fn, v.y = v.y * fo + x.y * fn;
             v.z = v.z * fo + x.z * fn, v.w = v.w * fo + x.w * fn;

@@ -9,11 +9,15 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from . import DGEN_EINVAL, DgenError, PagedCacheStruct, TokenRows, _check, _lib
+from . import DGEN_EINVAL, DgenError, PagedCacheStruct, _check, _lib
 
+_append, _attention = _lib.dgen_paged_append, _lib.dgen_paged_attention
+_pack = struct.Struct("Qqq").pack
+_stream_of = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() without the object around it
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1}
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
@@ -59,6 +63,9 @@ class PagedCache:
             page_table.data_ptr(), kv_len.data_ptr(), _CACHE_TYPES[k.dtype], *k.shape[:3], k.shape[3], self.batch,
             page_table.shape[1], stride)
         self._ref = ctypes.addressof(self._c)
+        self._dev = k.get_device()
+        self._scale = 1.0 / math.sqrt(self.head_dim)
+        self._row_types = _ROW_TYPES if e4m3 else (k.dtype,)
 
 
 def paged_workspace(device=None):
@@ -72,41 +79,40 @@ def paged_synchronize(workspace, stream: int | None = None) -> None:
     """Wait for the stream; raises DgenError (EDEVICE) if a device-side bounded wait ran out in a call with this
     workspace since the last check."""
     st = torch.cuda.current_stream(workspace.device).cuda_stream if stream is None else stream
-    _launch("dgen_paged_synchronize", workspace.device, workspace.data_ptr(), st)
+    _off_device("dgen_paged_synchronize", workspace.device, workspace.data_ptr(), st)
 
 
-def _rows(call, cache, name, t, tokens=None, heads=None, dtype=None):
-    """The C view of token rows [tokens][heads][head_dim]."""
-    _need(t.dim() == 3 and t.shape[2] == cache.head_dim and t.dtype in _ROW_TYPES and t.device == cache.device, call,
-          f"{name}: [tokens][heads][{cache.head_dim}] bf16 or fp16 on the cache's device")
-    _need((tokens is None or t.shape[0] == tokens) and (heads is None or t.shape[1] == heads) and
-          (dtype is None or t.dtype == dtype), call, f"{name}: shape {tuple(t.shape)} or {t.dtype} does not fit")
-    st, sh, se = t.stride()
-    _need(se == 1, call, f"{name}: the last dimension must be contiguous")
-    return TokenRows(t.data_ptr(), st, sh)
+def _bad(call: str, what: str):
+    raise DgenError(call, DGEN_EINVAL, what)
 
 
-def _common(call, cache, rows, cu_new, stream):
-    _need(cache.dtype in (rows.dtype, torch.float8_e4m3fn), call, f"{rows.dtype} rows, a cache of {cache.dtype}")
-    if cu_new is None:
-        _need(rows.shape[0] % cache.batch == 0, call, "without cu_new every sequence has the same number of rows")
-        cu = None
-    else:
-        _need(cu_new.shape == (cache.batch + 1,) and cu_new.dtype == torch.int32 and cu_new.is_contiguous() and
-              cu_new.device == cache.device, call, "cu_new: [batch + 1] int32 on the cache's device")
-        cu = cu_new.data_ptr()
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device).cuda_stream
-    return cu, stream
+def _check_rows(call, cache, name, t, shape, dtype):
+    """Raises for token rows that are not [tokens][heads][head_dim] of this shape, type and device."""
+    if t.dtype not in _ROW_TYPES:
+        _bad(call, f"{name}: rows are bf16 or fp16, not {t.dtype}")
+    if t.get_device() != cache._dev:
+        _bad(call, f"{name}: on {t.device}, the cache on {cache.device}")
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or t.stride(2) != 1:
+        _bad(call, f"{name}: wants [tokens][heads][{cache.head_dim}] with a contiguous last dimension")
+    if t.shape != shape or t.dtype != dtype:
+        _bad(call, f"{name}: {tuple(t.shape)} {t.dtype} where {tuple(shape)} {dtype} belongs")
+    _bad(call, f"{name}: does not fit the cache")
 
 
-def _launch(call, device, *args):
-    if device.index == torch.cuda.current_device():
+def _check_cu(call, cache, cu):
+    if cu.shape != (cache.batch + 1,) or cu.dtype != torch.int32 or not cu.is_contiguous() or \
+            cu.get_device() != cache._dev:
+        _bad(call, f"cu_new: wants [{cache.batch + 1}] int32 on the cache's device")
+
+
+def _off_device(call, device, *args):
+    with torch.cuda.device(device):
         _check(call, getattr(_lib, call)(*args))
-    else:
-        with torch.cuda.device(device):
-            _check(call, getattr(_lib, call)(*args))
 
+
+# The two calls below run once per layer and step of a serving loop, where their host time counts: the checks
+# are plain comparisons, messages are made only on failure, and a view of token rows goes to C as packed bytes
+# (struct dgen_token_rows).
 
 def paged_append(cache: PagedCache, k, v, q=None, q_out=None, cu_new=None, rope_base: float = 0.0,
                  stream: int | None = None) -> None:
@@ -114,19 +120,42 @@ def paged_append(cache: PagedCache, k, v, q=None, q_out=None, cu_new=None, rope_
     rope_base > 0 keys are rotated by their positions on the way, and queries q [tokens][heads][head_dim]
     into q_out (q_out may be q).  Rows belong to sequences by cu_new [batch + 1] (None: the same number
     each); see dgen_paged_append."""
-    call = "dgen_paged_append"
-    n = k.shape[0]
-    kr = _rows(call, cache, "k", k, heads=cache.n_kv_heads)
-    vr = _rows(call, cache, "v", v, n, cache.n_kv_heads, k.dtype)
-    _need((q is None) == (q_out is None), call, "q and q_out come together")
+    dev, dtype, shape, st = cache._dev, k.dtype, k.shape, k.stride()
+    if (len(shape) != 3 or shape[1] != cache.n_kv_heads or shape[2] != cache.head_dim or st[2] != 1 or
+            dtype not in cache._row_types or k.get_device() != dev):
+        _check_rows("dgen_paged_append", cache, "k", k, (shape[0] if len(shape) else 0, cache.n_kv_heads,
+                                                         cache.head_dim), dtype)
+    n = shape[0]
+    sv = v.stride()
+    if v.shape != shape or sv[2] != 1 or v.dtype != dtype or v.get_device() != dev:
+        _check_rows("dgen_paged_append", cache, "v", v, shape, dtype)
+    kr, vr = _pack(k.data_ptr(), st[0], st[1]), _pack(v.data_ptr(), sv[0], sv[1])
     heads, qr, qor = 0, None, None
     if q is not None:
-        heads = q.shape[1]
-        qr = ctypes.byref(_rows(call, cache, "q", q, n, None, k.dtype))
-        qor = ctypes.byref(_rows(call, cache, "q_out", q_out, n, heads, k.dtype))
-    cu, st = _common(call, cache, k, cu_new, stream)
-    _launch(call, cache.device, cache._ref, n, cu, _ROW_TYPES[k.dtype], ctypes.byref(kr), ctypes.byref(vr), heads, qr,
-            qor, rope_base, st)
+        if q_out is None:
+            _bad("dgen_paged_append", "q and q_out come together")
+        qs, sq, so = q.shape, q.stride(), q_out.stride()
+        if len(qs) != 3 or qs[0] != n or qs[2] != shape[2] or sq[2] != 1 or q.dtype != dtype or q.get_device() != dev:
+            _check_rows("dgen_paged_append", cache, "q", q, (n, qs[1] if len(qs) > 1 else 0, shape[2]), dtype)
+        if q_out.shape != qs or so[2] != 1 or q_out.dtype != dtype or q_out.get_device() != dev:
+            _check_rows("dgen_paged_append", cache, "q_out", q_out, qs, dtype)
+        heads = qs[1]
+        qr, qor = _pack(q.data_ptr(), sq[0], sq[1]), _pack(q_out.data_ptr(), so[0], so[1])
+    elif q_out is not None:
+        _bad("dgen_paged_append", "q and q_out come together")
+    cu = None
+    if cu_new is not None:
+        _check_cu("dgen_paged_append", cache, cu_new)
+        cu = cu_new.data_ptr()
+    elif n % cache.batch:
+        _bad("dgen_paged_append", "without cu_new every sequence has the same number of rows")
+    args = (cache._ref, n, cu, _ROW_TYPES[dtype], kr, vr, heads, qr, qor, rope_base,
+            _stream_of(dev) if stream is None else stream)
+    if dev != torch.cuda.current_device():
+        return _off_device("dgen_paged_append", cache.device, *args)
+    status = _append(*args)
+    if status:
+        raise DgenError("dgen_paged_append", status)
 
 
 def paged_attention(cache: PagedCache, q, out, workspace, cu_new=None, scale: float | None = None,
@@ -136,16 +165,33 @@ def paged_attention(cache: PagedCache, q, out, workspace, cu_new=None, scale: fl
     sequences' cached keys: scale (default 1 / sqrt(head_dim)), causal or all keys, a window of positions
     (0: none), scores capped as cap tanh(s / cap) (0: not), lse [tokens][heads] fp32 if given.  workspace:
     paged_workspace() of the cache's device; see dgen_paged_attention."""
-    call = "dgen_paged_attention"
-    qr = _rows(call, cache, "q", q)
-    n, heads = q.shape[0], q.shape[1]
-    outr = _rows(call, cache, "out", out, n, heads, q.dtype)
+    dev, dtype, shape, st, so = cache._dev, q.dtype, q.shape, q.stride(), out.stride()
+    if (len(shape) != 3 or shape[2] != cache.head_dim or st[2] != 1 or dtype not in cache._row_types or
+            q.get_device() != dev):
+        _check_rows("dgen_paged_attention", cache, "q", q,
+                    (*shape[:2], cache.head_dim) if len(shape) == 3 else (0, 0, cache.head_dim), dtype)
+    if out.shape != shape or so[2] != 1 or out.dtype != dtype or out.get_device() != dev:
+        _check_rows("dgen_paged_attention", cache, "out", out, shape, dtype)
+    n, heads = shape[0], shape[1]
+    lse_at = None
     if lse is not None:
-        _need(lse.shape == (n, heads) and lse.dtype == torch.float32 and lse.is_contiguous() and
-              lse.device == cache.device, call, "lse: [tokens][heads] fp32")
-    _need(workspace.dtype == torch.uint8 and workspace.is_contiguous() and workspace.device == cache.device, call,
-          "workspace: paged_workspace() of the cache's device")
-    cu, st = _common(call, cache, q, cu_new, stream)
-    _launch(call, cache.device, cache._ref, n, cu, _ROW_TYPES[q.dtype], heads, ctypes.byref(qr), ctypes.byref(outr),
-            1.0 / math.sqrt(cache.head_dim) if scale is None else scale, 1 if causal else 0, window, cap,
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), st)
+        if lse.shape != (n, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+            _bad("dgen_paged_attention", "lse: wants [tokens][heads] fp32 on the cache's device")
+        lse_at = lse.data_ptr()
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != dev:
+        _bad("dgen_paged_attention", "workspace: wants paged_workspace() of the cache's device")
+    cu = None
+    if cu_new is not None:
+        _check_cu("dgen_paged_attention", cache, cu_new)
+        cu = cu_new.data_ptr()
+    elif n % cache.batch:
+        _bad("dgen_paged_attention", "without cu_new every sequence has the same number of rows")
+    args = (cache._ref, n, cu, _ROW_TYPES[dtype], heads, _pack(q.data_ptr(), st[0], st[1]),
+            _pack(out.data_ptr(), so[0], so[1]), cache._scale if scale is None else scale, 1 if causal else 0, window,
+            cap, lse_at, workspace.data_ptr(), workspace.numel(),
+            _stream_of(dev) if stream is None else stream)
+    if dev != torch.cuda.current_device():
+        return _off_device("dgen_paged_attention", cache.device, *args)
+    status = _attention(*args)
+    if status:
+        raise DgenError("dgen_paged_attention", status)

@@ -521,7 +521,7 @@ int dgen_paged_append(const dgen_paged_cache* cache, int32_t n_tokens, const int
 /* Attention of the new tokens' (rotated) queries over their sequences' cached
  * keys, the new tokens' own included: per query head (KV head = head /
  * (n_q_heads / n_kv_heads)) and query at position p,
- *   out = sum_j softmax_j(f(scale q . k_j)) v_j,   f(s) = cap tanh(s / cap), or s for cap 0,
+ *   out = sum_j softmax_j(f(scale q . k_j)) v_j,   f(s) = cap tanh(s / cap), or s for cap 0, scale > 0,
  * over the keys j < kv_len with j <= p (causal 1) and |p - j| < window (0: no
  * window).  A row that sees no key gives zeros.  lse_or_null [tokens][n_q_heads]
  * fp32 receives the natural log of the softmax's sum (-inf for such a row), with

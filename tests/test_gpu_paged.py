@@ -146,10 +146,10 @@ def test_length_beyond_the_table_and_below_the_new_tokens(new, workspace):
 
 
 def test_large_scores_and_scale(workspace):
-    """Scores in the hundreds: one key takes all, no overflow; a negative scale."""
+    """Scores in the hundreds: one key takes all, no overflow; a scale of its own."""
     cache = make_cache("bf16", [500, 77], 2, 128, 16, seed=13, std=8.0)
     q = (16 * torch.randn(2, 8, 128, generator=_gen(14), device="cuda")).bfloat16()
-    for scale in (None, -0.1):
+    for scale in (None, 0.3):
         out = torch.empty_like(q)
         dg.paged_attention(cache, q, out, workspace, scale=scale)
         want, _, slack = ref.attention(cache, q, [1, 1], scale=scale)

@@ -58,7 +58,7 @@ def test_append_refuses(bad):
 
 @pytest.mark.parametrize("bad", [dict(n=-1), dict(n=3), dict(type=1), dict(type=2), dict(q=_rows(A + 2)),
                                  dict(out=_rows(ts=100)), dict(heads=3), dict(heads=0), dict(scale=math.inf),
-                                 dict(scale=math.nan), dict(causal=2), dict(window=-1), dict(cap=-1.0),
+                                 dict(scale=math.nan), dict(scale=0.0), dict(scale=-1.0), dict(causal=2), dict(window=-1), dict(cap=-1.0),
                                  dict(cap=math.nan), dict(cap=math.inf), dict(ws=None), dict(ws=A + 8),
                                  dict(n=1 << 30)])
 def test_attention_refuses(bad):
