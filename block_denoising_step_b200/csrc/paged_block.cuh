@@ -30,8 +30,7 @@
 // rounding per weight, averaged over the keys, below the output's own rounding.
 //
 // Keys behind the sequence's end and absent pages are not loaded; scores there
-// are replaced by -inf, and the V rows are zeroed before use (shared memory may
-// hold anything).  Every wait is bounded; on a timeout the kernel records an
+// are replaced by -inf, and the V rows are zeros (shared memory may hold anything).  Every wait is bounded; on a timeout the kernel records an
 // error, drains its own copies and MMAs, frees its tensor memory and exits.
 #pragma once
 
@@ -75,34 +74,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// The MMA warp stays converged and `issue` (set in one lane) predicates the
-// instructions themselves, so that the descriptors live in uniform registers:
-// issued from inside a one-lane branch, each product took 80 cycles of register
-// moves, more than its 64 on the tensor cores.
-// D (TMEM) (+)= A (shared memory) B^T (shared memory)
-__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                       uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
-        : "memory");
-}
 // D (TMEM) (+)= A (TMEM, K-major, two 16-bit values per column) x B (shared-memory descriptor)
-__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                       uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t issue, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(issue)
-        : "memory");
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -197,9 +181,6 @@ struct Parts {
         key = key_;
         id = lane < nbox && key < hi ? page_entry(c, b, key / c.page) : -1;
     }
-    __device__ __forceinline__ bool valid(const CacheView& c) const {
-        return static_cast<uint32_t>(id) < static_cast<uint32_t>(c.n_pages);
-    }
     __device__ __forceinline__ uint32_t row(const CacheView& c, int h) const {
         return id >= 0 ? row_in_page(c, id, h, key % c.page) : kNoRow;
     }
@@ -242,7 +223,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         mbar_init(ml_full, 4 * NG);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&piece_full[i], 1);
-            mbar_init(&piece_empty[i], 2 + 4 * NG);
+            mbar_init(&piece_empty[i], 2 + 4 * NG);  // producer, MMA issuer, softmax warps
         }
         fence_mbar_init();
     }
@@ -254,7 +235,8 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     pdl_enter();
-    const uint32_t tmem = *tmem_slot, t_s = tmem + L::T_S;
+    // all 512 columns are this CTA's, so its first column is column 0 (a constant base keeps the issue short)
+    constexpr uint32_t tmem = 0, t_s = L::T_S;
     const CacheView& c = a.c;
     const int br = 1 << log2_br, nbox = kBlkKeys >> log2_br;
 
@@ -282,6 +264,14 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             Piece q{};
             const bool have = walk.next(c, a.p, lane, q);
             q.end = !have;
+            if (have && q.n > 0) {  // is a page of its keys absent?
+                const int p0 = q.key0 / c.page, p1 = (min(q.key0 + q.n * kBlkKeys, q.hi) - 1) / c.page;
+                bool bad = false;
+#pragma unroll 4
+                for (int e = p0 + lane; e <= p1; e += 32)
+                    bad |= static_cast<uint32_t>(page_entry(c, q.b, e)) >= static_cast<uint32_t>(c.n_pages);
+                q.absent = __any_sync(0xffffffffu, bad);
+            }
             // what the join kernel has to know of the unit that starts here and goes on behind
             if (lane == 0 && (!have || (q.starts && !q.whole && q.rows > 0))) {
                 if (have || !cut) a.joins[blockIdx.x] = q;
@@ -310,17 +300,43 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         uint32_t ph = 0, pending = 0, fill_ph = 0;
         bool ok = true;
         int q_phase = -1;  // parity of the last Q copy issued
-        auto fetch = [&](const CUtensorMap* m, uint32_t row) {  // one K or V tile
-            const uint32_t have = __ballot_sync(0xffffffffu, row != kNoRow);
+        // One K or V tile of 128 keys from key k0 on, of which `row` is this lane's page part.  V rows that
+        // must not count (behind hi, absent pages) are zeroed here: a part that straddles hi is copied row
+        // by row instead of by TMA.
+        auto fetch = [&](const CUtensorMap* m, bool is_v, uint32_t row, int k0) {
+            const int live = min(s.hi - k0, kBlkKeys);
+            const bool straddles = is_v && row != kNoRow && (lane + 1) * br > live;
+            const uint32_t zero = is_v ? __ballot_sync(0xffffffffu, row == kNoRow && lane < nbox) : 0u;
+            const uint32_t part = is_v ? __ballot_sync(0xffffffffu, straddles) : 0u;  // one lane at most
+            const uint32_t have = __ballot_sync(0xffffffffu, row != kNoRow && !straddles);
 #pragma unroll
             for (int n = 0; n < L::NS; ++n) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ph ^ 1u, err, ERR_BLOCK_PRODUCER))) {
                     ok = false;
                     return;
                 }
+                if (zero | part) {
+                    constexpr int CH = L::SC / 8;  // 16-byte chunks of a stage row
+                    uint8_t* stage = smem + L::KV_OFF + st * L::STAGE;
+                    const int pl = part ? __ffs(part) - 1 : 0;
+                    const uint32_t prow = __shfl_sync(0xffffffffu, row, pl);
+                    for (int i = lane; i < kBlkKeys * CH; i += 32) {
+                        const int r = i / CH, ch = i % CH, box = r >> log2_br;
+                        const bool copy = part != 0 && box == pl;
+                        if (!copy && !((zero >> box) & 1u)) continue;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (copy && r < live)
+                            v = *reinterpret_cast<const uint4*>(
+                                c.v + (static_cast<size_t>(prow) + (r - (pl << log2_br))) * (HD * 2) + n * (L::SC * 2) + ch * 16);
+                        *reinterpret_cast<uint4*>(stage + (ch >> 3) * (kBlkKeys * 128) + r * 128 +
+                                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
                 if (lane == 0) mbar_expect_tx(&kv_full[st], __popc(have) * br * 128 * (L::SC / 64));
                 __syncwarp();
-                if (row != kNoRow) {
+                if ((have >> lane) & 1u) {
                     const uint32_t dst = sKV + st * L::STAGE + lane * br * 128;
 #pragma unroll
                     for (int x = 0; x < L::SC / 64; ++x)
@@ -360,12 +376,12 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 if (j < n) {
                     const uint32_t row = pk.row(c, h);
                     if (j + 1 < n) pk.ahead(c, s.b, key0 + (j + 1) * kBlkKeys, s.hi, nbox, lane);
-                    fetch(&tmK, row);
+                    fetch(&tmK, false, row, s.key0 + j * kBlkKeys);
                 }
                 if (ok && j >= 1 && j - 1 < n) {
                     const uint32_t row = pv.row(c, h);
                     if (j < n) pv.ahead(c, s.b, key0 + j * kBlkKeys, s.hi, nbox, lane);
-                    fetch(&tmV, row);
+                    fetch(&tmV, true, row, s.key0 + (j - 1) * kBlkKeys);
                 }
             }
             ++unit_no;
@@ -375,103 +391,86 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         for (int i = 0; i < ST; ++i)
             if ((pending >> i) & 1u) mbar_wait(&kv_full[i], (fill_ph >> i) & 1u, err, ERR_BLOCK_DRAIN);
     } else if (warp == 1) {
-        constexpr uint32_t type = BF ? (1u << 7) | (1u << 10) : 0u;  // operand types bf16 / f16
-        constexpr uint32_t base = (1u << 4) | type | (static_cast<uint32_t>(kBlkRows >> 4) << 24);
-        constexpr uint32_t idesc_s = base | (static_cast<uint32_t>(kBlkKeys >> 3) << 17);
-        constexpr uint32_t idesc_pv = base | (1u << 16) | (static_cast<uint32_t>(L::SC >> 3) << 17);
-        const uint32_t issue = lane == 0 ? 1u : 0u;
-        int st = 0, unit_no = 0, jj = 0;  // jj: tile counter of the CTA
-        uint32_t ph = 0;
-        bool ok = true;
-        auto take = [&](int& stage) -> bool {
-            if (!__all_sync(0xffffffffu, mbar_wait(&kv_full[st], ph, err, ERR_BLOCK_MMA))) return false;
-            tc_fence_after();
-            stage = st;
-            if (++st == ST) {
-                st = 0;
-                ph ^= 1u;
-            }
-            return true;
-        };
-        while (ok && next_piece()) {
-            const int n = s.n, key0 = s.key0;
-            if (n == 0) continue;
-            Parts pv;
-            pv.ahead(c, s.b, key0 + lane * br, s.hi, nbox, lane);
-            if (!__all_sync(0xffffffffu, mbar_wait(q_full, unit_no & 1, err, ERR_BLOCK_MMA))) break;
-            tc_fence_after();
-            auto issue_s = [&](int j) -> bool {  // S of the unit's tile j
-                const int buf = (jj + j) & 1;
+        // One elected thread issues everything.  A product of 128 x 128 x 16 takes 64 cycles, little more than
+        // its issue: what else this thread does, the tensor cores wait for.
+        if (elect_one()) {
+            constexpr uint32_t type = BF ? (1u << 7) | (1u << 10) : 0u;  // operand types bf16 / f16
+            constexpr uint32_t base = (1u << 4) | type | (static_cast<uint32_t>(kBlkRows >> 4) << 24);
+            constexpr uint32_t idesc_s = base | (static_cast<uint32_t>(kBlkKeys >> 3) << 17);
+            constexpr uint32_t idesc_pv = base | (1u << 16) | (static_cast<uint32_t>(L::SC >> 3) << 17);
+            int st = 0, unit_no = 0, jj = 0;  // jj: tile counter of the CTA
+            uint32_t ph = 0;
+            bool ok = true;
+            auto issue_s = [&](int buf) -> bool {  // the next K tile's scores
 #pragma unroll
                 for (int x = 0; x < L::NS; ++x) {
-                    int stage;
-                    if (!take(stage)) return false;
+                    if (!mbar_wait(&kv_full[st], ph, err, ERR_BLOCK_MMA)) return false;
+                    tc_fence_after();
                     const uint64_t ad0 = sdesc_sw128(sQ + x * (L::SC / 64) * (kBlkRows * 128));
-                    const uint64_t bd0 = sdesc_sw128(sKV + stage * L::STAGE);
+                    const uint64_t bd0 = sdesc_sw128(sKV + st * L::STAGE);
 #pragma unroll
                     for (int kk = 0; kk < L::SC / 16; ++kk) {
                         const int off = (kk >> 2) * (kBlkRows * 128 / 16) + 2 * (kk & 3);  // 16-byte units
-                        mma_ss(issue, t_s + buf * kBlkKeys, ad0 + off, bd0 + off, idesc_s, x > 0 || kk > 0 ? 1u : 0u);
+                        mma_bf16_ss(L::T_S + buf * kBlkKeys, ad0 + off, bd0 + off, idesc_s, x > 0 || kk > 0 ? 1u : 0u);
                     }
-                    commit(issue, &kv_empty[stage]);
+                    mma_commit(smem_u32(&kv_empty[st]));
+                    if (++st == ST) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
-                commit(issue, &s_full[buf]);
-                if (j == n - 1) commit(issue, q_empty);
+                mma_commit(smem_u32(&s_full[buf]));
                 return true;
             };
-            ok = issue_s(0) && (n < 2 || issue_s(1));
-            for (int j = 0; ok && j < n; ++j) {
-                const int t = jj + j, buf = t & 1, og = NG == 2 ? buf : 0;
-                const uint32_t have = __ballot_sync(0xffffffffu, pv.valid(c));
-                if (j + 1 < n) pv.ahead(c, s.b, key0 + (j + 1) * kBlkKeys + lane * br, s.hi, nbox, lane);
-                const int live = s.hi - (key0 + j * kBlkKeys);  // rows of the tile before the end
-                if (!__all_sync(0xffffffffu, mbar_wait(&p_full[buf], (t >> 1) & 1, err, ERR_BLOCK_MMA))) {
-                    ok = false;
-                    break;
-                }
-                if (j == 0 && unit_no > 0 &&
-                    !__all_sync(0xffffffffu, mbar_wait(o_free, (unit_no - 1) & 1, err, ERR_BLOCK_MMA))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t tp = t_s + buf * kBlkKeys + 64, t_o = tmem + og * HD;
-                const bool first = j < NG;  // nothing in this O yet
-#pragma unroll
-                for (int x = 0; x < L::NS; ++x) {
-                    int stage;
-                    if (!take(stage)) {
+            for (int i = 0; ok; ++i) {
+                const volatile Piece* q = reinterpret_cast<const volatile Piece*>(
+                    reinterpret_cast<const volatile uint8_t*>(s_piece) + (i & 1) * 64);
+                if (!mbar_wait(&piece_full[i & 1], (i >> 1) & 1, err, ERR_BLOCK_PIECE)) break;
+                const int n = q->n, end = q->end;
+                mbar_arrive(&piece_empty[i & 1]);
+                if (end) break;
+                if (n == 0) continue;
+                if (!mbar_wait(q_full, unit_no & 1, err, ERR_BLOCK_MMA)) break;
+                ok = issue_s(jj & 1) && (n < 2 || issue_s((jj + 1) & 1));
+                if (n <= 2) mma_commit(smem_u32(q_empty));
+                for (int j = 0; ok && j < n; ++j, ++jj) {
+                    const int buf = jj & 1;
+                    if (!mbar_wait(&p_full[buf], (jj >> 1) & 1, err, ERR_BLOCK_MMA) ||
+                        (j == 0 && unit_no > 0 && !mbar_wait(o_free, (unit_no - 1) & 1, err, ERR_BLOCK_MMA))) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sv = sKV + stage * L::STAGE;
-                    if (live < kBlkKeys || have != (nbox == 32 ? 0xFFFFFFFFu : (1u << nbox) - 1u)) {
-                        for (int r = lane; r < kBlkKeys; r += 32)
-                            if (r >= live || !((have >> (r >> log2_br)) & 1u))
+                    const uint32_t tp = L::T_S + buf * kBlkKeys + 64, t_o = NG == 2 ? buf * HD : 0;
+                    const uint32_t more = j >= NG ? 1u : 0u;  // (nothing in this O yet)
 #pragma unroll
-                                for (int e = 0; e < L::SC / 8; ++e)
-                                    *reinterpret_cast<uint4*>(smem + L::KV_OFF + stage * L::STAGE +
-                                                              (e >> 3) * (kBlkKeys * 128) + r * 128 + (e & 7) * 16) =
-                                        make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
+                    for (int x = 0; x < L::NS; ++x) {
+                        if (!mbar_wait(&kv_full[st], ph, err, ERR_BLOCK_MMA)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t vd0 = sdesc_sw128_mn(sKV + st * L::STAGE, kBlkKeys * 128);
+#pragma unroll
+                        for (int kk = 0; kk < kBlkKeys / 16; ++kk)
+                            mma_ts(t_o + x * L::SC, tp + kk * 8, vd0 + kk * (2048 / 16), idesc_pv, kk > 0 ? 1u : more);
+                        mma_commit(smem_u32(&kv_empty[st]));
+                        if (++st == ST) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
                     }
-                    const uint64_t vd0 = sdesc_sw128_mn(sv, kBlkKeys * 128);
-#pragma unroll
-                    for (int kk = 0; kk < kBlkKeys / 16; ++kk)
-                        mma_ts(issue, t_o + x * L::SC, tp + kk * 8, vd0 + kk * (2048 / 16), idesc_pv,
-                               !first || kk > 0 ? 1u : 0u);
-                    commit(issue, &kv_empty[stage]);
+                    if (!ok) break;
+                    mma_commit(smem_u32(&pv_done[buf]));
+                    if (j + 2 < n) {
+                        ok = issue_s(buf);
+                        if (j + 3 == n) mma_commit(smem_u32(q_empty));
+                    }
                 }
-                if (!ok) break;
-                commit(issue, &pv_done[buf]);
-                if (j + 2 < n) ok = issue_s(j + 2);
+                ++unit_no;
             }
-            jj += n;
-            ++unit_no;
+            mma_commit(smem_u32(drain));  // arrives when every MMA issued above has completed
+            mbar_wait(drain, 0, err, ERR_BLOCK_DRAIN);
         }
-        commit(issue, drain);  // arrives when every MMA issued above has completed
-        mbar_wait(drain, 0, err, ERR_BLOCK_DRAIN);
         __syncwarp();
     } else if (warp >= 4) {
         const int grp = NG == 2 ? (warp - 4) >> 2 : 0;
@@ -506,12 +505,15 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             float m_run = -INFINITY, l_run = 0.f;
             // this warpgroup's tiles: those whose CTA-wide number has its parity
             int j = NG == 2 ? ((jj & 1) == grp ? 0 : 1) : 0;
-            Parts pk;
-            pk.ahead(c, s.b, key0 + j * kBlkKeys + lane * br, s.hi, nbox, lane);
             for (; ok && j < n; j += NG) {
                 const int t = jj + j, buf = t & 1, k0 = key0 + j * kBlkKeys;
-                const uint32_t have = __ballot_sync(0xffffffffu, pk.valid(c));
-                if (j + NG < n) pk.ahead(c, s.b, k0 + NG * kBlkKeys + lane * br, s.hi, nbox, lane);
+                uint32_t have = all_parts;
+                if (s.absent) {  // which page parts are there
+                    const int key = k0 + lane * br;
+                    have = __ballot_sync(0xffffffffu, lane < nbox && key < s.hi &&
+                                                          static_cast<uint32_t>(page_entry(c, s.b, key / c.page)) <
+                                                              static_cast<uint32_t>(c.n_pages));
+                }
                 const uint32_t tb = t_s + buf * kBlkKeys + lane_off;
                 if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (t >> 1) & 1, err, ERR_BLOCK_SOFTMAX))) {
                     ok = false;
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(*tmem_slot, 512);
     }
 }
 

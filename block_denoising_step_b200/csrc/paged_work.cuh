@@ -150,6 +150,7 @@ struct Piece {
     int hi;              // keys from here on are not seen by any of its rows
     int whole, starts;   // the piece is the whole unit / holds the unit's first block
     int t_first, t_last; // teams that hold the unit's pieces
+    int absent;          // (block kernel) some page of its keys is absent
 };
 
 // A warp's walk over the units of its team's piece of the line.
