@@ -7,9 +7,9 @@
 // units of paged_work.cuh in blocks of 128 keys:
 //
 //   warp 2           scheduler: walks the units and hands each piece to the other
-//                    warps through shared memory, two in flight (warp 3 is idle);
-//   warp 0           producer: Q by one TMA box per 64 columns ([tokens][G] rows),
-//                    K and V in stages of 128 keys x SC columns (32 KB), one TMA box
+//                    warps through shared memory, two in flight;
+//   warps 0, 3       producers: Q by one TMA box per 64 columns ([tokens][G] rows),
+//                    K (warp 0) and V (warp 3) in stages of 128 keys x SC columns (32 KB), one TMA box
 //                    per page part (BR rows, a power of two that divides the page
 //                    size) and 64 columns, each lane issuing its own box;
 //   warp 1           MMA issuer: S = Q K^T (128 x 128 fp32) into one of two TMEM
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         mbar_init(ml_full, 4 * NG);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&piece_full[i], 1);
-            mbar_init(&piece_empty[i], 2 + 4 * NG);  // producer, MMA issuer, softmax warps
+            mbar_init(&piece_empty[i], 3 + 4 * NG);  // producers, MMA issuer, softmax warps
         }
         fence_mbar_init();
     }
@@ -290,20 +290,21 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             __syncwarp();
             if (!have) break;
         }
-    } else if (warp == 0) {
+    } else if (warp == 0 || warp == 3) {
+        const bool is_v = warp == 3;
+        const CUtensorMap* tm = is_v ? &tmV : &tmK;
         if (lane == 0) {
-            prefetch_tmap(&tmQ);
-            prefetch_tmap(&tmK);
-            prefetch_tmap(&tmV);
+            if (!is_v) prefetch_tmap(&tmQ);
+            prefetch_tmap(tm);
         }
-        int st = 0, unit_no = 0;
-        uint32_t ph = 0, pending = 0, fill_ph = 0;
+        int unit_no = 0, base = 0;  // base: stages of the ring used by the CTA's earlier pieces
+        uint32_t pending = 0, fill_ph = 0;
         bool ok = true;
         int q_phase = -1;  // parity of the last Q copy issued
-        // One K or V tile of 128 keys from key k0 on, of which `row` is this lane's page part.  V rows that
-        // must not count (behind hi, absent pages) are zeroed here: a part that straddles hi is copied row
-        // by row instead of by TMA.
-        auto fetch = [&](const CUtensorMap* m, bool is_v, uint32_t row, int k0) {
+        // This warp's tile of 128 keys from key k0 on into the ring from its stage number `at` on; `row` is
+        // this lane's page part.  V rows that must not count (behind hi, absent pages) are zeroed here: a part
+        // that straddles hi is copied row by row instead of by TMA.
+        auto fetch = [&](int at, uint32_t row, int k0) {
             const int live = min(s.hi - k0, kBlkKeys);
             const bool straddles = is_v && row != kNoRow && (lane + 1) * br > live;
             const uint32_t zero = is_v ? __ballot_sync(0xffffffffu, row == kNoRow && lane < nbox) : 0u;
@@ -311,6 +312,8 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             const uint32_t have = __ballot_sync(0xffffffffu, row != kNoRow && !straddles);
 #pragma unroll
             for (int n = 0; n < L::NS; ++n) {
+                const int st = (at + n) % ST;
+                const uint32_t ph = ((at + n) / ST) & 1;
                 if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ph ^ 1u, err, ERR_BLOCK_PRODUCER))) {
                     ok = false;
                     return;
@@ -340,56 +343,53 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     const uint32_t dst = sKV + st * L::STAGE + lane * br * 128;
 #pragma unroll
                     for (int x = 0; x < L::SC / 64; ++x)
-                        tma_load_2d(dst + x * (kBlkKeys * 128), m, n * L::SC + x * 64, static_cast<int>(row),
+                        tma_load_2d(dst + x * (kBlkKeys * 128), tm, n * L::SC + x * 64, static_cast<int>(row),
                                     smem_u32(&kv_full[st]));
                 }
                 pending |= 1u << st;
                 fill_ph = (fill_ph & ~(1u << st)) | (ph << st);
-                if (++st == ST) {
-                    st = 0;
-                    ph ^= 1u;
-                }
             }
         };
         while (ok && next_piece()) {
             const int h = s.h, n = s.n;
             if (n == 0) continue;
             const int key0 = s.key0 + lane * br;
-            if (unit_no > 0 &&
-                !__all_sync(0xffffffffu, mbar_wait(q_empty, (unit_no - 1) & 1, err, ERR_BLOCK_PRODUCER))) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) {
-                const int tok = s.first + s.row0 / a.p.G;
-                mbar_expect_tx(q_full, a.p.R * HD * 2);
+            if (!is_v) {
+                if (unit_no > 0 &&
+                    !__all_sync(0xffffffffu, mbar_wait(q_empty, (unit_no - 1) & 1, err, ERR_BLOCK_PRODUCER))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const int tok = s.first + s.row0 / a.p.G;
+                    mbar_expect_tx(q_full, a.p.R * HD * 2);
 #pragma unroll
-                for (int x = 0; x < HD / 64; ++x)
-                    tma_load_3d(sQ + x * (kBlkRows * 128), &tmQ, x * 64, h * a.p.G, tok, smem_u32(q_full));
-            }
-            q_phase = unit_no & 1;
-            Parts pk, pv;
-            pk.ahead(c, s.b, key0, s.hi, nbox, lane);
-            pv = pk;
-            // K0, K1, V0, K2, V1, ...
-            for (int j = 0; ok && j < n + 2; ++j) {
-                if (j < n) {
-                    const uint32_t row = pk.row(c, h);
-                    if (j + 1 < n) pk.ahead(c, s.b, key0 + (j + 1) * kBlkKeys, s.hi, nbox, lane);
-                    fetch(&tmK, false, row, s.key0 + j * kBlkKeys);
+                    for (int x = 0; x < HD / 64; ++x)
+                        tma_load_3d(sQ + x * (kBlkRows * 128), &tmQ, x * 64, h * a.p.G, tok, smem_u32(q_full));
                 }
-                if (ok && j >= 1 && j - 1 < n) {
-                    const uint32_t row = pv.row(c, h);
-                    if (j < n) pv.ahead(c, s.b, key0 + j * kBlkKeys, s.hi, nbox, lane);
-                    fetch(&tmV, true, row, s.key0 + (j - 1) * kBlkKeys);
-                }
+                q_phase = unit_no & 1;
             }
+            Parts parts;
+            parts.ahead(c, s.b, key0, s.hi, nbox, lane);
+            for (int j = 0; ok && j < n; ++j) {
+                // ring order K0, K1, V0, K2, V1, ..., V(n-2), V(n-1)
+                const int at = is_v ? j + min(n, j + 2) : (j < 2 ? j : 2 * j - 1);
+                const uint32_t row = parts.row(c, h);
+                if (j + 1 < n) parts.ahead(c, s.b, key0 + (j + 1) * kBlkKeys, s.hi, nbox, lane);
+                fetch(base + at * L::NS, row, s.key0 + j * kBlkKeys);
+            }
+            // (the ring's length times two: the phase is what counts)
+            base = (base + 2 * n * L::NS) % (2 * ST);
             ++unit_no;
         }
-        // our own copies land before the CTA goes away, consumed or not
-        if (q_phase >= 0) mbar_wait(q_full, q_phase, err, ERR_BLOCK_DRAIN);
-        for (int i = 0; i < ST; ++i)
-            if ((pending >> i) & 1u) mbar_wait(&kv_full[i], (fill_ph >> i) & 1u, err, ERR_BLOCK_DRAIN);
+        if (!ok) {
+            // let our own copies land before the CTA goes away (a stage that the other producer has filled since
+            // was consumed before: its wait only runs out).  Without a failure the MMA issuer has waited for
+            // every copy; if it alone gave up, it did so two seconds after the last of them.
+            if (q_phase >= 0) mbar_wait(q_full, q_phase, err, ERR_BLOCK_DRAIN);
+            for (int i = 0; i < ST; ++i)
+                if ((pending >> i) & 1u) mbar_wait(&kv_full[i], (fill_ph >> i) & 1u, err, ERR_BLOCK_DRAIN);
+        }
     } else if (warp == 1) {
         // One elected thread issues everything.  A product of 128 x 128 x 16 takes 64 cycles, little more than
         // its issue: what else this thread does, the tensor cores wait for.
