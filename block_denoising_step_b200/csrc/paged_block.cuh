@@ -11,7 +11,7 @@
 //   warps 0, 3       producers: Q by one TMA box per 64 columns ([tokens][G] rows),
 //                    K (warp 0) and V (warp 3) in stages of 128 keys x SC columns (32 KB), one TMA box
 //                    per page part (BR rows, a power of two that divides the page
-//                    size) and 64 columns, each lane issuing its own box;
+//                    size) and 64 columns;
 //   warp 1           MMA issuer: S = Q K^T (128 x 128 fp32) into one of two TMEM
 //                    buffers, O += P V with P from tensor memory (the upper 64 columns
 //                    of its S buffer) and V MN-major from shared memory;
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         }
         int unit_no = 0, base = 0;  // base: stages of the ring used by the CTA's earlier pieces
         uint32_t pending = 0, fill_ph = 0;
+        const bool leader = elect_one();
         bool ok = true;
         int q_phase = -1;  // parity of the last Q copy issued
         // This warp's tile of 128 keys from key k0 on into the ring from its stage number `at` on; `row` is
@@ -337,14 +338,18 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) mbar_expect_tx(&kv_full[st], __popc(have) * br * 128 * (L::SC / 64));
+                if (leader) mbar_expect_tx(&kv_full[st], __popc(have) * br * 128 * (L::SC / 64));
                 __syncwarp();
-                if ((have >> lane) & 1u) {
-                    const uint32_t dst = sKV + st * L::STAGE + lane * br * 128;
+                // (issued by one thread: copies of several lanes go out one by one at twice the cost)
+                for (uint32_t left = have; left != 0; left &= left - 1) {
+                    const int box = __ffs(left) - 1;
+                    const int r = static_cast<int>(__shfl_sync(0xffffffffu, row, box));
+                    const uint32_t dst = sKV + st * L::STAGE + (box << log2_br) * 128;
+                    if (leader) {
 #pragma unroll
-                    for (int x = 0; x < L::SC / 64; ++x)
-                        tma_load_2d(dst + x * (kBlkKeys * 128), tm, n * L::SC + x * 64, static_cast<int>(row),
-                                    smem_u32(&kv_full[st]));
+                        for (int x = 0; x < L::SC / 64; ++x)
+                            tma_load_2d(dst + x * (kBlkKeys * 128), tm, n * L::SC + x * 64, r, smem_u32(&kv_full[st]));
+                    }
                 }
                 pending |= 1u << st;
                 fill_ph = (fill_ph & ~(1u << st)) | (ph << st);
