@@ -12,17 +12,19 @@
 //                    K (warp 0) and V (warp 3) in stages of 128 keys x SC columns (32 KB), one TMA box
 //                    per page part (BR rows, a power of two that divides the page
 //                    size) and 64 columns;
-//   warp 1           MMA issuer: S = Q K^T (128 x 128 fp32) into one of two TMEM
+//   warp 1           MMA issuer: S = Q K^T (128 x 128 fp32) into one of NB TMEM
 //                    buffers, O += P V with P from tensor memory (the upper 64 columns
 //                    of its S buffer) and V MN-major from shared memory;
-//   4 or 8 warps     softmax: thread = query row.  One warpgroup takes every
-//                    tile at hd 256, where O fills half the tensor memory and the
-//                    products take longer than the exponentials; at hd <= 128 two
-//                    warpgroups take alternate tiles with an O, m and l each, joined
-//                    at the unit's end.
+//   8 warps          softmax: thread = query row.  Two warpgroups take alternate
+//                    tiles; the running maximum goes from one to the other through
+//                    shared memory as soon as a tile's is known, each keeps its own
+//                    sum, joined at the unit's end.
 //
-// Order of the products: S0, S1, P0 V0, S2, P1 V1, S3, ...: the softmax of one
-// tile runs beside the products of its neighbours.  Tiles of 128 keys, because
+// Order of the products, with NB score buffers: S0 .. S(NB-1), P0 V0, S(NB), P1 V1,
+// S(NB+1), ...: two tiles' softmax run beside the products of their neighbours.
+// hd <= 128 has room for a third buffer, so that a warpgroup finds its next scores
+// ready when it has finished a tile (with two, and an O of its own for each
+// warpgroup, it waited for P V and the next S: 2,700 cycles per tile at hd 128).  Tiles of 128 keys, because
 // S = Q K^T with N = 64 would read 6 KB of operands per 32 cycles, more than shared
 // memory delivers; with N = 128 it is 8 KB per 64.
 // P is rounded once to the operand type (bf16 / fp16): hi + lo parts as in the
@@ -48,22 +50,21 @@ template <int HD>
 struct BlockLayout {
     static constexpr int SC = HD < 128 ? HD : 128;    // columns of a stage
     static constexpr int NS = HD / SC;                // stages per K or V tile
-    static constexpr int NG = HD == 256 ? 1 : 2;      // softmax warpgroups
-    static constexpr int THREADS = 128 + NG * 128;
+    static constexpr int NB = HD == 256 ? 2 : 3;      // score buffers in tensor memory
+    static constexpr int THREADS = 384;               // four role warps, two warpgroups of softmax
     static constexpr int Q_BYTES = kBlkRows * HD * 2; // HD / 64 boxes of [128 rows x 128 B]
     static constexpr int STAGE = kBlkKeys * SC * 2;   // SC / 64 boxes of [128 rows x 128 B]
-    static constexpr int STAGES = HD == 256 ? 5 : (HD == 128 ? 5 : 8);
+    static constexpr int STAGES = HD == 64 ? 8 : 5;
     static constexpr int KV_OFF = Q_BYTES;
-    static constexpr int ML_OFF = KV_OFF + STAGES * STAGE;           // float2 ml[2][NG][128]: by unit parity
-    static constexpr int PIECE_OFF = ML_OFF + (NG == 2 ? 2 * NG * kBlkRows * 8 : 0);
+    static constexpr int M_OFF = KV_OFF + STAGES * STAGE;  // float m[2][128]: the running maximum, by tile parity
+    static constexpr int PIECE_OFF = M_OFF + 2 * kBlkRows * 4;
     static constexpr int BAR_OFF = PIECE_OFF + 2 * 64;
-    // q_full, q_empty, kv_full[ST], kv_empty[ST], s_full[2], p_full[2], pv_done[2], o_free, drain, ml_full,
-    // piece_full[2], piece_empty[2]
-    static constexpr int N_BARS = 2 + 2 * STAGES + 6 + 2 + 1 + 4;
+    // q_full, q_empty, kv_full[ST], kv_empty[ST], s_full[NB], p_full[NB], pv_done[NB], m_pub[2], l_full, l_read,
+    // o_free, drain, piece_full[2], piece_empty[2]
+    static constexpr int N_BARS = 2 + 2 * STAGES + 3 * NB + 2 + 4 + 4;
     static constexpr int SLOT_OFF = BAR_OFF + N_BARS * 8;            // TMEM base
     static constexpr int SMEM_BYTES = SLOT_OFF + 16 + 1024;          // + slack for 1024-byte alignment
-    static constexpr int T_S = NG * HD;                              // first S column
-    static_assert(T_S + 2 * kBlkKeys <= 512, "tensor memory");
+    static_assert(HD + NB * kBlkKeys <= 512, "tensor memory");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -192,19 +193,20 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmV, const AttendArgs a, int log2_br, int* __restrict__ err) {
     using L = BlockLayout<HD>;
     using H2 = Half2<BF>;
-    constexpr int NG = L::NG, ST = L::STAGES;
+    constexpr int NB = L::NB, ST = L::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem), sQ = sbase, sKV = sbase + L::KV_OFF;
-    float2* s_ml = reinterpret_cast<float2*>(smem + L::ML_OFF);
+    float* s_m = reinterpret_cast<float*>(smem + L::M_OFF);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + ST;
-    uint64_t *s_full = kv_empty + ST, *p_full = s_full + 2, *pv_done = p_full + 2, *o_free = pv_done + 2,
-             *drain = o_free + 1, *ml_full = drain + 1, *piece_full = ml_full + 1, *piece_empty = piece_full + 2;
-    static_assert(sizeof(Piece) <= 64, "piece slot");
-    volatile Piece* s_piece = reinterpret_cast<volatile Piece*>(smem + L::PIECE_OFF);  // 64 bytes apart
+    uint64_t *s_full = kv_empty + ST, *p_full = s_full + NB, *pv_done = p_full + NB, *m_pub = pv_done + NB;
+    uint64_t *l_full = m_pub + 2, *l_read = l_full + 1, *o_free = l_read + 1, *drain = o_free + 1, *piece_full = drain + 1;
+    uint64_t* piece_empty = piece_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    static_assert(sizeof(Piece) <= 64, "piece slot");
+    volatile Piece* s_piece = reinterpret_cast<volatile Piece*>(smem + L::PIECE_OFF);  // 64 bytes apart
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -213,17 +215,19 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
         }
-        mbar_init(o_free, 4 * NG);
+        mbar_init(o_free, 8);
         mbar_init(drain, 1);
-        mbar_init(ml_full, 4 * NG);
+        mbar_init(l_full, 8);
+        mbar_init(l_read, 8);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&m_pub[i], 4);
             mbar_init(&piece_full[i], 1);
-            mbar_init(&piece_empty[i], 3 + 4 * NG);  // producers, MMA issuer, softmax warps
+            mbar_init(&piece_empty[i], 3 + 8);  // producers, MMA issuer, softmax warps
         }
         fence_mbar_init();
     }
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     tc_fence_after();
     pdl_enter();
     // all 512 columns are this CTA's, so its first column is column 0 (a constant base keeps the issue short)
-    constexpr uint32_t tmem = 0, t_s = L::T_S;
+    constexpr uint32_t t_s = HD;
     const CacheView& c = a.c;
     const int br = 1 << log2_br, nbox = kBlkKeys >> log2_br;
 
@@ -377,8 +381,8 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             Parts parts;
             parts.ahead(c, s.b, key0, s.hi, nbox, lane);
             for (int j = 0; ok && j < n; ++j) {
-                // ring order K0, K1, V0, K2, V1, ..., V(n-2), V(n-1)
-                const int at = is_v ? j + min(n, j + 2) : (j < 2 ? j : 2 * j - 1);
+                // ring order K0, .., K(NB-1), V0, K(NB), V1, ..., V(n-2), V(n-1)
+                const int at = is_v ? j + min(n, j + NB) : (j < NB ? j : 2 * j - NB + 1);
                 const uint32_t row = parts.row(c, h);
                 if (j + 1 < n) parts.ahead(c, s.b, key0 + (j + 1) * kBlkKeys, s.hi, nbox, lane);
                 fetch(base + at * L::NS, row, s.key0 + j * kBlkKeys);
@@ -403,10 +407,12 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             constexpr uint32_t base = (1u << 4) | type | (static_cast<uint32_t>(kBlkRows >> 4) << 24);
             constexpr uint32_t idesc_s = base | (static_cast<uint32_t>(kBlkKeys >> 3) << 17);
             constexpr uint32_t idesc_pv = base | (1u << 16) | (static_cast<uint32_t>(L::SC >> 3) << 17);
-            int st = 0, unit_no = 0, jj = 0;  // jj: tile counter of the CTA
+            int st = 0, unit_no = 0;
+            int buf = 0, sbuf = 0;      // score buffers of the next P V and the next S
+            uint32_t p_ph = 0;          // phase of p_full[buf]
             uint32_t ph = 0;
             bool ok = true;
-            auto issue_s = [&](int buf) -> bool {  // the next K tile's scores
+            auto issue_s = [&]() -> bool {  // the next K tile's scores
 #pragma unroll
                 for (int x = 0; x < L::NS; ++x) {
                     if (!mbar_wait(&kv_full[st], ph, err, ERR_BLOCK_MMA)) return false;
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
 #pragma unroll
                     for (int kk = 0; kk < L::SC / 16; ++kk) {
                         const int off = (kk >> 2) * (kBlkRows * 128 / 16) + 2 * (kk & 3);  // 16-byte units
-                        mma_bf16_ss(L::T_S + buf * kBlkKeys, ad0 + off, bd0 + off, idesc_s, x > 0 || kk > 0 ? 1u : 0u);
+                        mma_bf16_ss(t_s + sbuf * kBlkKeys, ad0 + off, bd0 + off, idesc_s, x > 0 || kk > 0 ? 1u : 0u);
                     }
                     mma_commit(smem_u32(&kv_empty[st]));
                     if (++st == ST) {
@@ -424,7 +430,8 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                         ph ^= 1u;
                     }
                 }
-                mma_commit(smem_u32(&s_full[buf]));
+                mma_commit(smem_u32(&s_full[sbuf]));
+                if (++sbuf == NB) sbuf = 0;
                 return true;
             };
             for (int i = 0; ok; ++i) {
@@ -436,17 +443,16 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 if (end) break;
                 if (n == 0) continue;
                 if (!mbar_wait(q_full, unit_no & 1, err, ERR_BLOCK_MMA)) break;
-                ok = issue_s(jj & 1) && (n < 2 || issue_s((jj + 1) & 1));
-                if (n <= 2) mma_commit(smem_u32(q_empty));
-                for (int j = 0; ok && j < n; ++j, ++jj) {
-                    const int buf = jj & 1;
-                    if (!mbar_wait(&p_full[buf], (jj >> 1) & 1, err, ERR_BLOCK_MMA) ||
+                for (int j = 0; ok && j < n && j < NB; ++j) ok = issue_s();
+                if (n <= NB) mma_commit(smem_u32(q_empty));
+                for (int j = 0; ok && j < n; ++j) {
+                    if (!mbar_wait(&p_full[buf], p_ph, err, ERR_BLOCK_MMA) ||
                         (j == 0 && unit_no > 0 && !mbar_wait(o_free, (unit_no - 1) & 1, err, ERR_BLOCK_MMA))) {
                         ok = false;
                         break;
                     }
-                    const uint32_t tp = L::T_S + buf * kBlkKeys + 64, t_o = NG == 2 ? buf * HD : 0;
-                    const uint32_t more = j >= NG ? 1u : 0u;  // (nothing in this O yet)
+                    const uint32_t tp = t_s + buf * kBlkKeys + 64;
+                    const uint32_t more = j > 0 ? 1u : 0u;  // (nothing in O yet)
 #pragma unroll
                     for (int x = 0; x < L::NS; ++x) {
                         if (!mbar_wait(&kv_full[st], ph, err, ERR_BLOCK_MMA)) {
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                         const uint64_t vd0 = sdesc_sw128_mn(sKV + st * L::STAGE, kBlkKeys * 128);
 #pragma unroll
                         for (int kk = 0; kk < kBlkKeys / 16; ++kk)
-                            mma_ts(t_o + x * L::SC, tp + kk * 8, vd0 + kk * (2048 / 16), idesc_pv, kk > 0 ? 1u : more);
+                            mma_ts(x * L::SC, tp + kk * 8, vd0 + kk * (2048 / 16), idesc_pv, kk > 0 ? 1u : more);
                         mma_commit(smem_u32(&kv_empty[st]));
                         if (++st == ST) {
                             st = 0;
@@ -466,9 +472,13 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     }
                     if (!ok) break;
                     mma_commit(smem_u32(&pv_done[buf]));
-                    if (j + 2 < n) {
-                        ok = issue_s(buf);
-                        if (j + 3 == n) mma_commit(smem_u32(q_empty));
+                    if (++buf == NB) {
+                        buf = 0;
+                        p_ph ^= 1u;
+                    }
+                    if (j + NB < n) {
+                        ok = issue_s();  // over the scores and weights of the tile just multiplied
+                        if (j + NB + 1 == n) mma_commit(smem_u32(q_empty));
                     }
                 }
                 ++unit_no;
@@ -478,12 +488,11 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         }
         __syncwarp();
     } else if (warp >= 4) {
-        const int grp = NG == 2 ? (warp - 4) >> 2 : 0;
-        const int quarter = warp & 3;  // TMEM lanes this warp may access
+        const int grp = (warp - 4) >> 2;  // takes the tiles of its parity
+        const int quarter = warp & 3;     // TMEM lanes this warp may access
         const int row = quarter * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t t_o = tmem + (NG == 2 ? grp * HD : 0) + lane_off;
-        constexpr int C = NG == 2 ? 32 : 64;  // score columns in registers (168 or 255 a thread)
+        constexpr int C = 32;  // score columns in registers (168 a thread)
         const float fac = a.scale * kLog2e, inv_cap = a.cap > 0.f ? kLn2 / a.cap : 0.f;
         const uint32_t all_parts = (1u << nbox) - 1u;
         // tanh's coefficients for raw scores: c_i (fac inv_cap)^(2i)
@@ -497,8 +506,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 f *= w2;
             }
         }
-        int jj = 0;
-        int unit_no = 0;
+        int jj = 0, unit_no = 0;  // jj: tile counter of the CTA
         bool ok = true;
         while (ok && next_piece()) {
             const int h = s.h, n = s.n, row0 = s.row0, rows = s.rows, key0 = s.key0;
@@ -507,11 +515,13 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             visible(s.pos0 + (row0 + min(row, rows - 1)) / a.p.G, s.len, a.p.causal, a.p.window, vlo, vhi);
             // keys every row of this warp sees (ranges only move up with the row)
             const int all_lo = __shfl_sync(0xffffffffu, vlo, 31), all_hi = __shfl_sync(0xffffffffu, vhi, 0);
-            float m_run = -INFINITY, l_run = 0.f;
-            // this warpgroup's tiles: those whose CTA-wide number has its parity
-            int j = NG == 2 ? ((jj & 1) == grp ? 0 : 1) : 0;
-            for (; ok && j < n; j += NG) {
-                const int t = jj + j, buf = t & 1, k0 = key0 + j * kBlkKeys;
+            float m_run = -INFINITY, l_run = 0.f;  // the maximum this warp's l is relative to
+            // the slots of m are free once every warp has read the sums of the unit before
+            if (n > 0 && unit_no > 0 &&
+                !__all_sync(0xffffffffu, mbar_wait(l_read, (unit_no - 1) & 1, err, ERR_BLOCK_SOFTMAX)))
+                break;
+            for (int j = (jj ^ grp) & 1; ok && j < n; j += 2) {
+                const int t = jj + j, buf = t % NB, k0 = key0 + j * kBlkKeys;
                 uint32_t have = all_parts;
                 if (s.absent) {  // which page parts are there
                     const int key = k0 + lane * br;
@@ -520,7 +530,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                                                               static_cast<uint32_t>(c.n_pages));
                 }
                 const uint32_t tb = t_s + buf * kBlkKeys + lane_off;
-                if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (t >> 1) & 1, err, ERR_BLOCK_SOFTMAX))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], (t / NB) & 1, err, ERR_BLOCK_SOFTMAX))) {
                     ok = false;
                     break;
                 }
@@ -554,18 +564,30 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     if (raw > -INFINITY)
                         mt = small ? capped_small(mt, mt * inv_cap) : capped_any(mt * inv_cap, kLog2e * a.cap);
                 }
-                const bool move = mt > m_run + kRescale || (m_run == -INFINITY && mt > -INFINITY);
-                float corr = 1.f;
-                if (move) {
-                    corr = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
-                    l_run *= corr;
-                    m_run = mt;
+                // the maximum after the tile before this one, from the other warpgroup
+                float m_prev = -INFINITY;
+                if (j > 0) {
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(&m_pub[(t - 1) & 1], ((t - 1) >> 1) & 1, err, ERR_BLOCK_SOFTMAX))) {
+                        ok = false;
+                        break;
+                    }
+                    m_prev = s_m[((t - 1) & 1) * kBlkRows + row];
+                }
+                const bool move = mt > m_prev + kRescale || (m_prev == -INFINITY && mt > -INFINITY);
+                const float m_new = move ? mt : m_prev;
+                s_m[(t & 1) * kBlkRows + row] = m_new;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m_pub[t & 1]);
+                if (m_new != m_run) {
+                    l_run *= m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
+                    m_run = m_new;
                 }
                 const float mu = m_run == -INFINITY ? 0.f : m_run;
-                if (__any_sync(0xffffffffu, move && j >= NG)) {  // rescale O rows, after the P V before this one
-                    const int tp = t - NG;
-                    if (!__all_sync(0xffffffffu,
-                                    mbar_wait(&pv_done[tp & 1], (tp >> 1) & 1, err, ERR_BLOCK_SOFTMAX))) {
+                if (__any_sync(0xffffffffu, move && j > 0)) {  // rescale O rows, after the P V before this one
+                    const float corr = move ? (m_prev == -INFINITY ? 0.f : ex2(m_prev - m_new)) : 1.f;
+                    if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(t - 1) % NB], ((t - 1) / NB) & 1, err,
+                                                           ERR_BLOCK_SOFTMAX))) {
                         ok = false;
                         break;
                     }
@@ -573,11 +595,11 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
 #pragma unroll 1
                     for (int col = 0; col < HD; col += 32) {
                         uint32_t r[32];
-                        tmem_ld32(t_o + col, r);
+                        tmem_ld32(col + lane_off, r);
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * corr);
-                        tmem_st32(t_o + col, r);
+                        tmem_st32(col + lane_off, r);
                     }
                     tmem_st_wait();
                 }
@@ -598,7 +620,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             ls[e & 1] = add2(ls[e & 1], pair(p0, p1));
                             p[e] = H2::pack(p0, p1);
                         }
-                    } else if (small && !cut) {  // capped_small in pairs, its powers of 1 / cap in the coefficients
+                    } else if (small) {  // capped_small in pairs, its powers of 1 / cap in the coefficients
 #pragma unroll
                         for (int e = 0; e < C / 2; ++e) {
                             const f32x2 v = pair(x[2 * e], x[2 * e + 1]), z = mul2(v, v);
@@ -608,7 +630,11 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             q = fma2(z, q, pair(tc[0], tc[0]));
                             q = fma2(z, q, pair(1.f, 1.f));
                             const float2 y = unpair(fma2(mul2(v, fac2), q, nmu2));
-                            const float p0 = ex2(y.x), p1 = ex2(y.y);
+                            float p0 = ex2(y.x), p1 = ex2(y.y);
+                            if (cut) {
+                                p0 = x[2 * e] == -INFINITY ? 0.f : p0;
+                                p1 = x[2 * e + 1] == -INFINITY ? 0.f : p1;
+                            }
                             ls[e & 1] = add2(ls[e & 1], pair(p0, p1));
                             p[e] = H2::pack(p0, p1);
                         }
@@ -637,60 +663,51 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[buf]);
             }
-            // the unit's last products
-            for (int e = 1; ok && e <= 2 && e <= n; ++e) {
-                const int tp = jj + n - e;
-                ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[tp & 1], (tp >> 1) & 1, err, ERR_BLOCK_SOFTMAX));
-            }
             if (!ok) break;
-            tc_fence_after();
-            jj += n;
-            float f0 = 1.f, f1 = 0.f, m = m_run, l = l_run;
-            bool has0 = n > 0, has1 = false;
-            if constexpr (NG == 2) {
-                // (two sets of s_ml in turn: who writes the next but one has seen all arrive at the next)
-                float2* ml = s_ml + (unit_no & 1) * (NG * kBlkRows);
-                ml[grp * kBlkRows + row] = make_float2(m_run, l_run);
+            // The unit's maximum is the last tile's; both warpgroups' sums relative to it.  They change hands in
+            // the slots of m, which the two threads of a row alone use and have read by then.
+            float m = -INFINITY, l = 0.f;
+            if (n > 0) {
+                const int last = jj + n - 1, own = (last & 1) == grp;
+                m = m_run;
+                if (!own) {
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(&m_pub[last & 1], (last >> 1) & 1, err, ERR_BLOCK_SOFTMAX)))
+                        break;
+                    m = s_m[(last & 1) * kBlkRows + row];
+                    l_run *= m_run == -INFINITY ? 1.f : ex2(m_run - m);
+                }
+                s_m[((last + own) & 1) * kBlkRows + row] = l_run;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ml_full);
-                if (!__all_sync(0xffffffffu, mbar_wait(ml_full, unit_no & 1, err, ERR_BLOCK_SOFTMAX))) break;
+                if (lane == 0) mbar_arrive(l_full);
+                if (!__all_sync(0xffffffffu, mbar_wait(l_full, unit_no & 1, err, ERR_BLOCK_SOFTMAX))) break;
+                l = l_run + s_m[((last + 1 - own) & 1) * kBlkRows + row];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(l_read);
+                if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[last % NB], (last / NB) & 1, err, ERR_BLOCK_SOFTMAX)))
+                    break;
+                tc_fence_after();
+                jj += n;
                 ++unit_no;
-                const float2 A = ml[row], B = ml[kBlkRows + row];
-                const int j_first = (jj - n) & 1;  // the group of the unit's first tile
-                has0 = n > 1 || (n == 1 && j_first == 0);
-                has1 = n > 1 || (n == 1 && j_first == 1);
-                m = fmaxf(A.x, B.x);
-                f0 = A.x == -INFINITY ? 1.f : ex2(A.x - m);
-                f1 = B.x == -INFINITY ? 1.f : ex2(B.x - m);
-                l = A.y * f0 + B.y * f1;
             }
             const bool whole = s.whole, live = row < rows;
             const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.starts ? 1 : 0);
-            const int c_begin = NG == 2 ? grp * (HD / 2) : 0, c_end = c_begin + HD / NG;
-            const uint32_t to = tmem + lane_off;
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            const int tok = s.first + (row0 + row) / a.p.G, head = h * a.p.G + (row0 + row) % a.p.G;
+            // half of the columns each; a piece that saw no key leaves (-inf, 0) alone
+            const int c_end = n == 0 && !whole ? grp * (HD / 2) + 1 : (grp + 1) * (HD / 2);
 #pragma unroll 1
-            for (int col = c_begin; col < c_end; col += 32) {
-                if (n == 0 && !whole && col > 0) break;  // nothing seen: (-inf, 0) alone
+            for (int col = grp * (HD / 2); col < c_end; col += 32) {
                 float v[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                uint32_t r[32];
-                if (has0) {
-                    tmem_ld32(to + col, r);
+                if (n > 0) {
+                    tmem_ld32(col + lane_off, reinterpret_cast<uint32_t(&)[32]>(v));
                     tmem_ld_wait();
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * f0;
-                }
-                if (NG == 2 && has1) {
-                    tmem_ld32(to + HD + col, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] += __uint_as_float(r[e]) * f1;
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 }
                 if (!live) continue;
                 if (whole) {
-                    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-                    const int tok = s.first + (row0 + row) / a.p.G, head = h * a.p.G + (row0 + row) % a.p.G;
                     uint4* dst = reinterpret_cast<uint4*>(a.out.p + (tok * a.out.ts + head * a.out.hs + col) * 2);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
