@@ -202,12 +202,13 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
             !encode_16bit(&tv, a.c.v, 2, kdims, kstrides, kbox))
             return DGEN_EINVAL;
     }
-    // teams of 4 or 2 row tiles where the average sequence's tiles fill them to 7/8
+    // teams of 4 or 2 row tiles where the average sequence's tiles fill them to 7/8; of 2 at most for a ragged
+    // batch, whose last teams have idle members
     const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
     const int64_t avg = std::max<int64_t>(1, (rows / a.c.B + a.p.R - 1) / a.p.R);
     a.p.TS = 1;
     for (int ts : {4, 2})
-        if (a.p.TS == 1 && 8 * avg >= 7 * ((avg + ts - 1) / ts * ts)) a.p.TS = ts;
+        if (a.p.TS == 1 && (ts == 2 || !a.c.cu) && 8 * avg >= 7 * ((avg + ts - 1) / ts * ts)) a.p.TS = ts;
     const int64_t units = std::min<int64_t>(rows, rows / (a.p.R * a.p.TS) + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + 2 * paged::kBlkKeys - 2) / paged::kBlkKeys;
     if (units * blocks >= INT32_MAX) return DGEN_EINVAL;

@@ -60,8 +60,8 @@ struct BlockLayout {
     static constexpr int PIECE_OFF = M_OFF + 2 * kBlkRows * 4;
     static constexpr int BAR_OFF = PIECE_OFF + 2 * 64;
     // q_full, q_empty, kv_full[ST], kv_empty[ST], s_full[NB], p_full[NB], pv_done[NB], m_pub[2], l_full, l_read,
-    // o_free, drain, piece_full[2], piece_empty[2]
-    static constexpr int N_BARS = 2 + 2 * STAGES + 3 * NB + 2 + 4 + 4;
+    // o_free, drain, tail, piece_full[2], piece_empty[2]
+    static constexpr int N_BARS = 2 + 2 * STAGES + 3 * NB + 2 + 5 + 4;
     static constexpr int SLOT_OFF = BAR_OFF + N_BARS * 8;            // TMEM base
     static constexpr int SMEM_BYTES = SLOT_OFF + 16 + 1024;          // + slack for 1024-byte alignment
     static_assert(HD + NB * kBlkKeys <= 512, "tensor memory");
@@ -103,12 +103,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// C scores of each of this warp's rows
-template <int C>
-__device__ __forceinline__ void load_scores(uint32_t taddr, float (&x)[C]) {
-#pragma unroll
-    for (int e = 0; e < C; e += 32) tmem_ld32(taddr + e, reinterpret_cast<uint32_t(&)[32]>(x[e]));
-    tmem_ld_wait();
+// 32 scores of each of this warp's rows: the load is started, and waited for, apart
+// (the wait names the registers, so that nothing reads them before it)
+__device__ __forceinline__ void scores_start(uint32_t taddr, float (&x)[32]) {
+    tmem_ld32(taddr, reinterpret_cast<uint32_t(&)[32]>(x));
+}
+__device__ __forceinline__ void scores_wait(float (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
+                   "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]),
+                   "+f"(x[15]), "+f"(x[16]), "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]),
+                   "+f"(x[22]), "+f"(x[23]), "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]),
+                   "+f"(x[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(x[30]), "+f"(x[31]));
 }
 // two fp32 values in one register pair: packed arithmetic halves the instructions
 // of the softmax, which shares its issue slots with the exponentials
@@ -138,6 +147,16 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // bits [lo, hi) of a 32-bit word whose bit 0 is position `base`
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int base) {
     const int a = min(max(lo - base, 0), 32), b = min(max(hi - base, 0), 32);
@@ -145,24 +164,20 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int base) {
     return up & ~dn;
 }
 
-// Masks C scores of the tile's columns c0 .. (keys k0 ..): outside [lo, hi), or in
+// Masks 32 scores of the tile's columns c0 .. (keys k0 ..): outside [lo, hi), or in
 // an absent page part.
-template <int C>
-__device__ __forceinline__ void mask_scores(float (&x)[C], int lo, int hi, int k0, int c0, uint32_t have, int log2_br) {
-#pragma unroll
-    for (int q = 0; q < C; q += 32) {
-        uint32_t parts = 0;
-        if (log2_br >= 5) {
-            parts = (have >> ((c0 + q) >> log2_br)) & 1u ? 0xFFFFFFFFu : 0u;
-        } else {
-            const uint32_t one = (1u << (1 << log2_br)) - 1u;
-            for (int e = 0; e < 32; e += 1 << log2_br) parts |= (have >> ((c0 + q + e) >> log2_br)) & 1u ? one << e : 0u;
-        }
-        const uint32_t bits = range_bits(lo, hi, k0 + q) & parts;
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (!((bits >> e) & 1u)) x[q + e] = -INFINITY;
+__device__ __forceinline__ void mask_scores(float (&x)[32], int lo, int hi, int k0, int c0, uint32_t have, int log2_br) {
+    uint32_t parts = 0;
+    if (log2_br >= 5) {
+        parts = (have >> (c0 >> log2_br)) & 1u ? 0xFFFFFFFFu : 0u;
+    } else {
+        const uint32_t one = (1u << (1 << log2_br)) - 1u;
+        for (int e = 0; e < 32; e += 1 << log2_br) parts |= (have >> ((c0 + e) >> log2_br)) & 1u ? one << e : 0u;
     }
+    const uint32_t bits = range_bits(lo, hi, k0) & parts;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!((bits >> e) & 1u)) x[e] = -INFINITY;
 }
 
 // Partial results of this kernel: [slot][hd / 4][128 rows] float4, so that a warp
@@ -201,8 +216,8 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
     uint64_t *q_full = bars, *q_empty = bars + 1, *kv_full = bars + 2, *kv_empty = kv_full + ST;
     uint64_t *s_full = kv_empty + ST, *p_full = s_full + NB, *pv_done = p_full + NB, *m_pub = pv_done + NB;
-    uint64_t *l_full = m_pub + 2, *l_read = l_full + 1, *o_free = l_read + 1, *drain = o_free + 1, *piece_full = drain + 1;
-    uint64_t* piece_empty = piece_full + 2;
+    uint64_t *l_full = m_pub + 2, *l_read = l_full + 1, *o_free = l_read + 1, *drain = o_free + 1, *tail = drain + 1;
+    uint64_t *piece_full = tail + 1, *piece_empty = piece_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     static_assert(sizeof(Piece) <= 64, "piece slot");
@@ -222,6 +237,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         }
         mbar_init(o_free, 8);
         mbar_init(drain, 1);
+        mbar_init(tail, 1);
         mbar_init(l_full, 8);
         mbar_init(l_read, 8);
         for (int i = 0; i < 2; ++i) {
@@ -302,19 +318,16 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             prefetch_tmap(tm);
         }
         int unit_no = 0, base = 0;  // base: stages of the ring used by the CTA's earlier pieces
-        uint32_t pending = 0, fill_ph = 0;
+        uint32_t pending = 0, fill_ph = 0, tail_ph = 0;
         const bool leader = elect_one();
         bool ok = true;
         int q_phase = -1;  // parity of the last Q copy issued
         // This warp's tile of 128 keys from key k0 on into the ring from its stage number `at` on; `row` is
-        // this lane's page part.  V rows that must not count (behind hi, absent pages) are zeroed here: a part
-        // that straddles hi is copied row by row instead of by TMA.
+        // this lane's page part.  V rows that must not count (behind hi, absent pages) are cleared here.
         auto fetch = [&](int at, uint32_t row, int k0) {
             const int live = min(s.hi - k0, kBlkKeys);
-            const bool straddles = is_v && row != kNoRow && (lane + 1) * br > live;
-            const uint32_t zero = is_v ? __ballot_sync(0xffffffffu, row == kNoRow && lane < nbox) : 0u;
-            const uint32_t part = is_v ? __ballot_sync(0xffffffffu, straddles) : 0u;  // one lane at most
-            const uint32_t have = __ballot_sync(0xffffffffu, row != kNoRow && !straddles);
+            const uint32_t have = __ballot_sync(0xffffffffu, row != kNoRow);
+            const uint32_t absent = ~have & ((1u << nbox) - 1u);
 #pragma unroll
             for (int n = 0; n < L::NS; ++n) {
                 const int st = (at + n) % ST;
@@ -323,26 +336,10 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     ok = false;
                     return;
                 }
-                if (zero | part) {
-                    constexpr int CH = L::SC / 8;  // 16-byte chunks of a stage row
-                    uint8_t* stage = smem + L::KV_OFF + st * L::STAGE;
-                    const int pl = part ? __ffs(part) - 1 : 0;
-                    const uint32_t prow = __shfl_sync(0xffffffffu, row, pl);
-                    for (int i = lane; i < kBlkKeys * CH; i += 32) {
-                        const int r = i / CH, ch = i % CH, box = r >> log2_br;
-                        const bool copy = part != 0 && box == pl;
-                        if (!copy && !((zero >> box) & 1u)) continue;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (copy && r < live)
-                            v = *reinterpret_cast<const uint4*>(
-                                c.v + (static_cast<size_t>(prow) + (r - (pl << log2_br))) * (HD * 2) + n * (L::SC * 2) + ch * 16);
-                        *reinterpret_cast<uint4*>(stage + (ch >> 3) * (kBlkKeys * 128) + r * 128 +
-                                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
-                if (leader) mbar_expect_tx(&kv_full[st], __popc(have) * br * 128 * (L::SC / 64));
+                // rows to clear: the copies then report to a barrier of their own, and kv_full follows the clearing
+                const bool clear = is_v && (live < kBlkKeys || absent != 0);
+                uint64_t* done = clear ? tail : &kv_full[st];
+                if (leader) mbar_expect_tx(done, __popc(have) * br * 128 * (L::SC / 64));
                 __syncwarp();
                 // (issued by one thread: copies of several lanes go out one by one at twice the cost)
                 for (uint32_t left = have; left != 0; left &= left - 1) {
@@ -352,11 +349,28 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     if (leader) {
 #pragma unroll
                         for (int x = 0; x < L::SC / 64; ++x)
-                            tma_load_2d(dst + x * (kBlkKeys * 128), tm, n * L::SC + x * 64, r, smem_u32(&kv_full[st]));
+                            tma_load_2d(dst + x * (kBlkKeys * 128), tm, n * L::SC + x * 64, r, smem_u32(done));
                     }
                 }
                 pending |= 1u << st;
                 fill_ph = (fill_ph & ~(1u << st)) | (ph << st);
+                if (clear) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(tail, tail_ph, err, ERR_BLOCK_PRODUCER))) {
+                        ok = false;
+                        return;
+                    }
+                    tail_ph ^= 1u;
+                    constexpr int CH = L::SC / 8;  // 16-byte chunks of a stage row (which is cleared whole: no swizzle)
+                    for (int i = lane; i < kBlkKeys * CH; i += 32) {
+                        const int r = i / CH, ch = i % CH;
+                        if (r >= live || ((absent >> (r >> log2_br)) & 1u))
+                            *reinterpret_cast<uint4*>(smem + L::KV_OFF + st * L::STAGE + (ch >> 3) * (kBlkKeys * 128) +
+                                                      r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (leader) mbar_arrive(&kv_full[st]);
+                }
             }
         };
         while (ok && next_piece()) {
@@ -492,16 +506,15 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         const int quarter = warp & 3;     // TMEM lanes this warp may access
         const int row = quarter * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-        constexpr int C = 32;  // score columns in registers (168 a thread)
         const float fac = a.scale * kLog2e, inv_cap = a.cap > 0.f ? kLn2 / a.cap : 0.f;
         const uint32_t all_parts = (1u << nbox) - 1u;
-        // tanh's coefficients for raw scores: c_i (fac inv_cap)^(2i)
-        float tc[5];
+        // tanh's coefficients for raw scores: fac c_i w^(2i + 2), w = fac inv_cap
+        float tc[4];
         {
             const float w = fac * inv_cap, w2 = w * w;
-            float f = w2;
+            float f = fac * w2;
 #pragma unroll
-            for (int i = 0; i < 5; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 tc[i] = kTanhCoef[i] * f;
                 f *= w2;
             }
@@ -535,25 +548,33 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                // maximum of the raw scores (scale > 0 and the cap keep their order), C columns at a
-                // time; the last C stay in registers
+                // maximum of the raw scores (scale > 0 and the cap keep their order), 32 columns at a time, the
+                // next 32 on their way meanwhile
                 const bool cut = have != all_parts || k0 < all_lo || k0 + kBlkKeys > all_hi;
-                float x[C];
+                float xa[32], xb[32];
                 float mx[4], mn = INFINITY;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
-#pragma unroll 1
-                for (int c0 = 0; c0 < kBlkKeys; c0 += C) {
-                    load_scores<C>(tb + c0, x);
+                auto look = [&](float(&x)[32], int c0) {
                     if constexpr (CAP) {
                         float lo[4] = {mn, x[1], x[2], x[3]};
 #pragma unroll
-                        for (int e = 0; e < C; ++e) lo[e & 3] = fminf(lo[e & 3], x[e]);
+                        for (int e = 0; e < 16; ++e) lo[e & 3] = min3(lo[e & 3], x[2 * e], x[2 * e + 1]);
                         mn = fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3]));
                     }
-                    if (cut) mask_scores<C>(x, vlo, vhi, k0 + c0, c0, have, log2_br);
+                    if (cut) mask_scores(x, vlo, vhi, k0 + c0, c0, have, log2_br);
 #pragma unroll
-                    for (int e = 0; e < C; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
+                    for (int e = 0; e < 16; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
+                };
+                scores_start(tb, xa);
+#pragma unroll 1
+                for (int c0 = 0; c0 < kBlkKeys; c0 += 64) {
+                    scores_wait(xa);
+                    scores_start(tb + c0 + 32, xb);
+                    look(xa, c0);
+                    scores_wait(xb);
+                    scores_start(tb + 64, xa);  // (the second time for the weights)
+                    look(xb, c0 + 32);
                 }
                 const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 bool small = false;
@@ -605,16 +626,12 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 }
                 f32x2 ls[2] = {0ull, 0ull};
                 const f32x2 fac2 = pair(fac, fac), nmu2 = pair(-mu, -mu);
-#pragma unroll 1
-                for (int c0 = kBlkKeys - C; c0 >= 0; c0 -= C) {
-                    if (c0 < kBlkKeys - C) {
-                        load_scores<C>(tb + c0, x);
-                        if (cut) mask_scores<C>(x, vlo, vhi, k0 + c0, c0, have, log2_br);
-                    }
-                    uint32_t p[C / 2];
+                // P of 32 columns c0 .. over columns 64 + c0 / 2 .. of S_j, whose scores have been read by then
+                auto weigh = [&](float(&x)[32], int c0) {
+                    uint32_t p[16];
                     if constexpr (!CAP) {
 #pragma unroll
-                        for (int e = 0; e < C / 2; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float2 y = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), fac2, nmu2));
                             const float p0 = ex2(y.x), p1 = ex2(y.y);
                             ls[e & 1] = add2(ls[e & 1], pair(p0, p1));
@@ -622,14 +639,12 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                         }
                     } else if (small) {  // capped_small in pairs, its powers of 1 / cap in the coefficients
 #pragma unroll
-                        for (int e = 0; e < C / 2; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const f32x2 v = pair(x[2 * e], x[2 * e + 1]), z = mul2(v, v);
-                            f32x2 q = fma2(z, pair(tc[4], tc[4]), pair(tc[3], tc[3]));
-                            q = fma2(z, q, pair(tc[2], tc[2]));
+                            f32x2 q = fma2(z, pair(tc[3], tc[3]), pair(tc[2], tc[2]));
                             q = fma2(z, q, pair(tc[1], tc[1]));
                             q = fma2(z, q, pair(tc[0], tc[0]));
-                            q = fma2(z, q, pair(1.f, 1.f));
-                            const float2 y = unpair(fma2(mul2(v, fac2), q, nmu2));
+                            const float2 y = unpair(fma2(mul2(v, z), q, fma2(v, fac2, nmu2)));
                             float p0 = ex2(y.x), p1 = ex2(y.y);
                             if (cut) {
                                 p0 = x[2 * e] == -INFINITY ? 0.f : p0;
@@ -641,7 +656,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     } else {
                         const float cap2 = kLog2e * a.cap;
 #pragma unroll
-                        for (int e = 0; e < C / 2; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             float pe[2];
 #pragma unroll
                             for (int w = 0; w < 2; ++w) {
@@ -652,9 +667,21 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             p[e] = H2::pack(pe[0], pe[1]);
                         }
                     }
-                    // P of columns c0 .. over columns 64 + c0 / 2 .. of S_j, whose scores have been read by now
-#pragma unroll
-                    for (int e = 0; e < C / 2; e += 16) tmem_st16(tb + 64 + c0 / 2 + e, p + e);
+                    tmem_st16(tb + 64 + c0 / 2, p);
+                };
+                // columns 96 .., 64 .., 32 .., 0 ..
+#pragma unroll 1
+                for (int c0 = 64; c0 >= 0; c0 -= 64) {
+                    weigh(xb, c0 + 32);
+                    scores_wait(xa);
+                    if (c0 > 0) scores_start(tb + 32, xb);
+                    if (cut) mask_scores(xa, vlo, vhi, k0 + c0, c0, have, log2_br);
+                    weigh(xa, c0);
+                    if (c0 > 0) {
+                        scores_wait(xb);
+                        scores_start(tb, xa);
+                        if (cut) mask_scores(xb, vlo, vhi, k0 + 32, 32, have, log2_br);
+                    }
                 }
                 const float2 lsum = unpair(add2(ls[0], ls[1]));
                 l_run += lsum.x + lsum.y;
