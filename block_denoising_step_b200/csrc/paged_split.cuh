@@ -11,7 +11,7 @@
 // (16 keys x 8 rows per instruction), O^T += V^T P^T.  P^T's operand layout is
 // S^T's accumulator layout transposed 8 x 8 (movmatrix).  P is kept as hi + lo
 // 16-bit parts (about 16 significant bits), so the output's own rounding is the
-// only one that shows.
+// only one that shows; with an E4M3 cache and bf16 rows fp16's 11 bits alone do.
 //
 // Memory-bound: every visible K and V row is read once.  Each warp streams its
 // own tiles of 16 or 32 keys through a private ring of shared memory (cp.async 16 bytes,
@@ -38,8 +38,11 @@ template <int HD, int ES, int NT>
 struct SplitLayout {
     static constexpr int ROWB = HD * ES;        // bytes of a cache row
     static constexpr int CH = ROWB / 16;        // 16-byte chunks of a row
-    // 16-key steps per warp tile: 8 KB of K and V where registers allow
-    static constexpr int MT = NT == 1 && ROWB <= 128 ? 2 : 1;
+    // 16-key steps per warp tile
+    static constexpr int MT = NT == 1 && ROWB == 64 ? 2 : 1;
+    // CTAs per SM: short rows need more warps than long ones to keep as many bytes in flight, and a tile's chain
+    // of dependent steps (scores, maximum, weights, products) overlapped
+    static constexpr int CTAS = ROWB <= 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : ROWB == 256 ? 2 : 1;
     static constexpr int KEYS = 16 * MT;                      // keys per warp tile
     static constexpr int BLOCK_KEYS = kSplitWarps * KEYS;     // keys per block of the line
     static constexpr int TILE = KEYS * ROWB;
@@ -51,14 +54,21 @@ struct SplitSmem {
     using L = SplitLayout<HD, ES, NT>;
     static constexpr int R = 8 * NT;
     static constexpr int OP = HD + 4;  // padded row of the join buffers
-    static constexpr int JOIN = kSplitWarps * R * OP * 4;
-    static constexpr int Q_OFF = L::RING > JOIN ? L::RING : JOIN;
-    static constexpr int QS_OFF = Q_OFF + R * HD * 2;             // float qscale[R]
-    static constexpr int ML_OFF = QS_OFF + R * 4;                 // float m[W][R], l[W][R]
+    static constexpr int JOIN = kSplitWarps / 2 * R * OP * 4;
+    static constexpr int REST = 2 * R * HD * 2 + 2 * R * 4 + 2 * kSplitWarps * R * 4 + kSplitWarps * L::STAGES * 4 + 16 +
+                                2 * 64 + 32 * static_cast<int>(sizeof(Walk));
+    // The next unit's first tiles are fetched before the current one is joined, where a join buffer beside the
+    // ring costs no CTA of the SM (227 KB, 1 KB each); else the join uses the ring's memory.
+    static constexpr bool EARLY = L::RING + JOIN + REST <= 227 * 1024 / L::CTAS - 1024;
+    static constexpr int JOIN_OFF = EARLY ? L::RING : 0;
+    static constexpr int Q_OFF = EARLY ? L::RING + JOIN : (L::RING > JOIN ? L::RING : JOIN);
+    static constexpr int Q_BYTES = R * HD * 2;                    // two in turn
+    static constexpr int QS_OFF = Q_OFF + 2 * Q_BYTES;            // float qscale[2][R]
+    static constexpr int ML_OFF = QS_OFF + 2 * R * 4;             // float m[W][R], l[W][R]
     static constexpr int MASK_OFF = ML_OFF + 2 * kSplitWarps * R * 4;  // uint32 mask[W][STAGES]
     static constexpr int FLAG_OFF = MASK_OFF + kSplitWarps * L::STAGES * 4;
-    static constexpr int PIECE_OFF = FLAG_OFF + 16;                     // the current piece
-    static constexpr int WALK_OFF = PIECE_OFF + 64;                     // Walk[32]: warp 0's, a lane each
+    static constexpr int PIECE_OFF = FLAG_OFF + 16;                     // the current piece and the next
+    static constexpr int WALK_OFF = PIECE_OFF + 2 * 64;                 // Walk[32]: warp 0's, a lane each
     static constexpr int BYTES = (WALK_OFF + 32 * static_cast<int>(sizeof(Walk)) + 15) & ~15;
 };
 
@@ -91,10 +101,17 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v) {
     return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
 
+// old value of *p, which goes on to old + 1, from `last` to 0
+__device__ __forceinline__ unsigned inc_acq_rel(unsigned* p, unsigned last) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(last) : "memory");
+    return old;
+}
+
 // HD: head size.  ES: bytes of a cache element.  BF: the products run in bf16
 // (else fp16; always fp16 for E4M3 caches).  NT: tiles of 8 query rows.
 template <int HD, int ES, bool BF, int NT>
-__global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTAS) paged_split_kernel(const AttendArgs a) {
     using L = SplitLayout<HD, ES, NT>;
     using S = SplitSmem<HD, ES, NT>;
     using H2 = Half2<BF>;
@@ -102,84 +119,78 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
     constexpr uint32_t kAllKeys = KEYS == 32 ? 0xFFFFFFFFu : (1u << KEYS) - 1u;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const uint32_t sbase = smem_u32(smem), ring = sbase + warp * (ST * 2 * L::TILE), sq = sbase + S::Q_OFF;
-    float* qscale = reinterpret_cast<float*>(smem + S::QS_OFF);
+    const uint32_t sbase = smem_u32(smem), ring = sbase + warp * (ST * 2 * L::TILE);
     float* s_m = reinterpret_cast<float*>(smem + S::ML_OFF);
     float* s_l = s_m + kSplitWarps * R;
     uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + S::MASK_OFF) + warp * ST;
     int* s_flag = reinterpret_cast<int*>(smem + S::FLAG_OFF);
-    float* join = reinterpret_cast<float*>(smem);
+    float* join = reinterpret_cast<float*>(smem + S::JOIN_OFF);
 
     pdl_enter();
     const CacheView& c = a.c;
-    // warp 0 walks the units; its state waits in shared memory, not in the registers of the key loop
     static_assert(sizeof(Piece) <= 64, "piece slot");
-    Piece& piece = *reinterpret_cast<Piece*>(smem + S::PIECE_OFF);
-    if (warp == 0) {
-        Walk walk;
-        walk.start(c, a.p, lane, a.min_blocks, blockIdx.x, a.n_ctas);
-        reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane] = walk;
-    }
-    for (;;) {
-        if (warp == 0) {
-            Walk walk = reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane];
-            Piece q{};
-            q.end = !walk.next(c, a.p, lane, q);
-            reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane] = walk;
-            if (lane == 0) piece = q;
+    auto slot_of = [&](int i) { return reinterpret_cast<Piece*>(smem + S::PIECE_OFF + i * 64); };
+    // warp 0 walks the units; its state waits in shared memory, not in the registers of the key loop
+    auto walk_on = [&](int i) {
+        const volatile Walk& seen = reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane];
+        if (seen.t >= seen.t_end) {
+            if (lane == 0) slot_of(i)->end = 1;
+            return;
         }
-        __syncthreads();
-        const Piece s = piece;
-        if (s.end) break;
-        const int h = s.h, row0 = s.row0, rows = s.rows;
-        const int key_first = s.key0 + warp * KEYS;
-        const int n_tiles = s.n;
+        Walk walk = reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane];
+        Piece q{};
+        q.end = !walk.next(c, a.p, lane, q);
+        reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane] = walk;
+        if (lane == 0) *slot_of(i) = q;
+    };
 
-        // rows of the next tile to fetch: table entry loaded one tile ahead
-        int key_next = key_first + (lane & (KEYS - 1));
-        int id_next = key_next < s.hi ? page_entry(c, s.b, key_next / c.page) : -1;
-        auto fetch = [&](int stage, bool live) {
-            uint32_t row = kNoRow;
-            if (live && key_next < s.hi) row = row_in_page(c, id_next, h, key_next % c.page);
-            key_next += L::BLOCK_KEYS;
-            id_next = live && key_next < s.hi ? page_entry(c, s.b, key_next / c.page) : -1;
-            const uint32_t mask = __ballot_sync(0xffffffffu, row != kNoRow) & kAllKeys;
-            if (lane == 0) s_mask[stage] = mask;
-            if (mask != 0) {
-                const uint32_t dk = ring + stage * (2 * L::TILE), dv = dk + L::TILE;
+    // Fetching: rows of this warp's next tile; the table entry is loaded one tile ahead.
+    int key_next = 0, id_next = -1;
+    auto fetch = [&](const Piece& p, int stage, bool live) {
+        uint32_t row = kNoRow;
+        if (live && key_next < p.hi) row = row_in_page(c, id_next, p.h, key_next % c.page);
+        key_next += L::BLOCK_KEYS;
+        id_next = live && key_next < p.hi ? page_entry(c, p.b, key_next / c.page) : -1;
+        const uint32_t mask = __ballot_sync(0xffffffffu, row != kNoRow) & kAllKeys;
+        if (lane == 0) s_mask[stage] = mask;
+        if (mask != 0) {
+            const uint32_t dk = ring + stage * (2 * L::TILE), dv = dk + L::TILE;
 #pragma unroll
-                for (int i = 0; i < KEYS * CH / 32; ++i) {
-                    const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
-                    const uint32_t src = __shfl_sync(0xffffffffu, row, r);
-                    const bool ok = src != kNoRow;
-                    const size_t off = ok ? static_cast<size_t>(src) * L::ROWB + ch * 16 : 0;
-                    const uint32_t d = r * L::ROWB + swz_chunk<CH>(r, ch) * 16;
-                    attn::cp_async16(dk + d, c.k + off, ok);
-                    attn::cp_async16(dv + d, c.v + off, ok);
-                }
+            for (int i = 0; i < KEYS * CH / 32; ++i) {
+                const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                const bool ok = src != kNoRow;
+                const size_t off = ok ? static_cast<size_t>(src) * L::ROWB + ch * 16 : 0;
+                const uint32_t d = r * L::ROWB + swz_chunk<CH>(r, ch) * 16;
+                attn::cp_async16(dk + d, c.k + off, ok);
+                attn::cp_async16(dv + d, c.v + off, ok);
             }
-            attn::cp_commit();
-        };
+        }
+        attn::cp_commit();
+    };
+    // The first tiles of a piece, and its queries into Q buffer i, one warp per row.
+    auto begin = [&](const Piece& p, int i) {
+        key_next = p.key0 + warp * KEYS + (lane & (KEYS - 1));
+        id_next = key_next < p.hi ? page_entry(c, p.b, key_next / c.page) : -1;
 #pragma unroll
-        for (int i = 0; i < ST - 1; ++i) fetch(i, i < n_tiles);
-
-        // queries -> shared memory, one warp per row
+        for (int e = 0; e < ST - 1; ++e) fetch(p, e, e < p.n);
+        float* qscale = reinterpret_cast<float*>(smem + S::QS_OFF) + i * R;
         for (int r = warp; r < R; r += kSplitWarps) {
             constexpr int PER = HD / 32;  // elements per lane: 2, 4 or 8
             uint32_t w[PER / 2];
 #pragma unroll
             for (int e = 0; e < PER / 2; ++e) w[e] = 0;
-            if (r < rows) {
-                const int tok = s.first + (row0 + r) / a.p.G, head = h * a.p.G + (row0 + r) % a.p.G;
-                const uint8_t* p = a.q.p + (tok * a.q.ts + head * a.q.hs + lane * PER) * 2;
+            if (r < p.rows) {
+                const int tok = p.first + (p.row0 + r) / a.p.G, head = p.h * a.p.G + (p.row0 + r) % a.p.G;
+                const uint8_t* src = a.q.p + (tok * a.q.ts + head * a.q.hs + lane * PER) * 2;
                 if constexpr (PER == 8) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(p);
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
                     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
                 } else if constexpr (PER == 4) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p);
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
                     w[0] = v.x, w[1] = v.y;
                 } else {
-                    w[0] = *reinterpret_cast<const uint32_t*>(p);
+                    w[0] = *reinterpret_cast<const uint32_t*>(src);
                 }
             }
             if constexpr (ES == 2) {
@@ -211,10 +222,28 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                     el = blk + ((x >> 1) & 1) * 8 + (x >> 2) * 2;
                 }
                 const int ch = el >> 3;
-                *reinterpret_cast<uint32_t*>(smem + S::Q_OFF + r * (HD * 2) + swz_chunk<QCH>(r, ch) * 16 +
-                                             (el & 7) * 2) = w[e];
+                *reinterpret_cast<uint32_t*>(smem + S::Q_OFF + i * S::Q_BYTES + r * (HD * 2) +
+                                             swz_chunk<QCH>(r, ch) * 16 + (el & 7) * 2) = w[e];
             }
         }
+    };
+
+    if (warp == 0) {
+        Walk walk;
+        walk.start(c, a.p, lane, a.min_blocks, blockIdx.x, a.n_ctas);
+        reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane] = walk;
+        walk_on(0);
+    }
+    __syncthreads();
+    Piece s = *slot_of(0);
+    if (!s.end) begin(s, 0);
+    for (int cur = 0; !s.end; cur ^= 1) {
+        if (warp == 0) walk_on(cur ^ 1);
+        const int h = s.h, row0 = s.row0, rows = s.rows;
+        const int key_first = s.key0 + warp * KEYS;
+        const int n_tiles = s.n;
+        const uint32_t sq = sbase + S::Q_OFF + cur * S::Q_BYTES;
+        const float* qscale = reinterpret_cast<const float*>(smem + S::QS_OFF) + cur * R;
 
         // visible range and score factor of this thread's rows (columns 2 t4, 2 t4 + 1 of each tile)
         int vlo[NT][2], vhi[NT][2];
@@ -233,7 +262,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                 const int r = min(nt * 8 + 2 * t4 + j, rows - 1);
                 visible(s.pos0 + (row0 + r) / a.p.G, s.len, a.p.causal, a.p.window, vlo[nt][j], vhi[nt][j]);
             }
-        __syncthreads();  // queries staged
+        __syncthreads();  // queries and the next piece are there, the join's memory is free
         const float kscale = ES == 1 ? __ldg(c.k_scale + h) : 1.f;
         float fac[NT][2];
 #pragma unroll
@@ -393,6 +422,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                     }
                 }
                 uint32_t ph[MT][NT][2], pl[MT][NT][2];
+                const bool low = ES == 2 || !a.q_bf16;
 #pragma unroll
                 for (int km = 0; km < MT; ++km)
 #pragma unroll
@@ -409,7 +439,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                             const uint32_t hi = H2::pack(p[2 * half], p[2 * half + 1]);
                             const float2 hf = H2::unpack(hi);
                             ph[km][nt][half] = movmatrix_t(hi);
-                            pl[km][nt][half] = movmatrix_t(H2::pack(p[2 * half] - hf.x, p[2 * half + 1] - hf.y));
+                            if (low) pl[km][nt][half] = movmatrix_t(H2::pack(p[2 * half] - hf.x, p[2 * half + 1] - hf.y));
                         }
                     }
                 // O^T += V^T P^T
@@ -440,16 +470,15 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                                 uint32_t va[4];
 #pragma unroll
                                 for (int half = 0; half < 2; ++half) {
-                                    const uint32_t v = x[2 * half + u];
-                                    const uint32_t e0 = e4m3x2_f16x2(static_cast<uint16_t>(v));
-                                    const uint32_t e1 = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
-                                    va[2 * half] = __byte_perm(e0, e1, 0x5410);      // byte 2g: row g
-                                    va[2 * half + 1] = __byte_perm(e0, e1, 0x7632);  // byte 2g + 1: row g + 8
+                                    // bytes 2g, 2g + 1 of key 2t, then of key 2t + 1: rows g and g + 8
+                                    const uint32_t v = __byte_perm(x[2 * half + u], 0, 0x3120);
+                                    va[2 * half] = e4m3x2_f16x2(static_cast<uint16_t>(v));
+                                    va[2 * half + 1] = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
                                 }
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
                                     mma_16816<BF>(o[2 * mp + u][nt], va, ph[km][nt][0], ph[km][nt][1]);
-                                    mma_16816<BF>(o[2 * mp + u][nt], va, pl[km][nt][0], pl[km][nt][1]);
+                                    if (low) mma_16816<BF>(o[2 * mp + u][nt], va, pl[km][nt][0], pl[km][nt][1]);
                                 }
                             }
                         }
@@ -457,11 +486,14 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                 }
             }
             __syncwarp();  // every lane has read stage `stage` and its mask
-            fetch((i + ST - 1) % ST, i + ST - 1 < n_tiles);
+            fetch(s, (i + ST - 1) % ST, i + ST - 1 < n_tiles);
         }
         attn::cp_wait<0>();
+        const Piece following = *slot_of(cur ^ 1);
+        if (S::EARLY && !following.end) begin(following, cur ^ 1);
 
-        // join the four warps: m, then scaled O and l
+        // join the four warps: m and l, then O scaled to the common m: two warps' in memory, on which the other
+        // two add
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -473,25 +505,32 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
                     s_l[warp * R + nt * 8 + 2 * t4 + j] = l_run[nt][j];
                 }
             }
-        __syncthreads();  // all warps are past their rings
+        __syncthreads();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int pass = 0; pass < 2; ++pass) {
+            if ((warp >> 1) != pass) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = nt * 8 + 2 * t4 + j;
-                const float f = m_run[nt][j] == -INFINITY
-                                    ? 0.f
-                                    : exp2f(m_run[nt][j] - fmaxf(fmaxf(s_m[r], s_m[R + r]),
-                                                                 fmaxf(s_m[2 * R + r], s_m[3 * R + r])));
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int mt = 0; mt < HD / 16; ++mt)
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = nt * 8 + 2 * t4 + j;
+                        const float f = m_run[nt][j] == -INFINITY
+                                            ? 0.f
+                                            : exp2f(m_run[nt][j] - fmaxf(fmaxf(s_m[r], s_m[R + r]),
+                                                                         fmaxf(s_m[2 * R + r], s_m[3 * R + r])));
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int col = ES == 2 ? mt * 16 + g + 8 * half : mt * 16 + 2 * g + half;
-                        join[(warp * R + r) * S::OP + col] = o[mt][nt][2 * half + j] * f;
+                        for (int mt = 0; mt < HD / 16; ++mt)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int col = ES == 2 ? mt * 16 + g + 8 * half : mt * 16 + 2 * g + half;
+                                float& to = join[((warp & 1) * R + r) * S::OP + col];
+                                const float v = o[mt][nt][2 * half + j] * f;
+                                to = pass == 0 ? v : to + v;
+                            }
                     }
             }
-        __syncthreads();
+            __syncthreads();
+        }
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.starts ? 1 : 0);
         const bool out_bf = ES == 2 ? BF : a.q_bf16 != 0;
         const float vscale = ES == 1 ? __ldg(c.v_scale + h) : 1.f;
@@ -501,9 +540,12 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
             const float m = fmaxf(fmaxf(s_m[r], s_m[R + r]), fmaxf(s_m[2 * R + r], s_m[3 * R + r]));
             float l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kSplitWarps; ++w) {
+            for (int w = 0; w < 2; ++w) {
                 const float4 x = *reinterpret_cast<const float4*>(join + (w * R + r) * S::OP + col);
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+#pragma unroll
+            for (int w = 0; w < kSplitWarps; ++w) {
                 // (a warp without a maximum has l = 0, or NaN from NaN scores)
                 l += s_l[w * R + r] * (s_m[w * R + r] == -INFINITY ? 1.f : exp2f(s_m[w * R + r] - m));
             }
@@ -515,17 +557,20 @@ __global__ void __launch_bounds__(kSplitWarps * 32) paged_split_kernel(const Att
             }
         }
         if (!s.whole) {
+            // (the barrier orders all threads' stores before thread 0's release, and its acquire before their loads)
             const unsigned last = s.t_last - s.t_first;
-            __threadfence();
             __syncthreads();
-            if (threadIdx.x == 0) *s_flag = atomicInc(a.counters + s.t_first, last) == last;
+            if (threadIdx.x == 0) *s_flag = inc_acq_rel(a.counters + s.t_first, last) == last;
             __syncthreads();
             if (*s_flag) {  // every piece of this unit is in memory; the counter is back at zero
-                __threadfence();
                 join_pieces<HD>(a, s, 0, out_bf, vscale, 0, rows, threadIdx.x, kSplitWarps * 32);
             }
         }
-        __syncthreads();  // join buffers free before the next unit's copies
+        if (!S::EARLY && !following.end) {
+            __syncthreads();  // the join's memory is the ring's
+            begin(following, cur ^ 1);
+        }
+        s = following;
     }
 }
 

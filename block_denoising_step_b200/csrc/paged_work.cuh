@@ -4,7 +4,8 @@
 // The n_b * G query rows that share a KV head of a sequence are cut into row tiles
 // of R; TS neighbouring row tiles form a unit (sequence, KV head, super tile), whose
 // keys are dealt in blocks of KB.  All units' blocks, in unit order, form one line
-// of T blocks, cut into equal pieces, one per team of TS CTAs; member m of a team
+// of T blocks, cut into equal pieces, one per team of TS CTAs (where units are
+// few or short, each is cut by itself or not at all); member m of a team
 // computes row tile m of each unit, so that the team reads the same keys at the same
 // time and all but one member find them in L2 (separate units per CTA read them from
 // HBM once per row tile: 1.2 GB instead of 0.3 for eight canvases over 4096 tokens).
@@ -32,7 +33,7 @@ struct SeqInfo {
     int lo, blocks;    // irregular: first key and blocks of every unit
     int regular;       // units have ranges of their own (prefix_blocks)
     int b;
-    int head;          // blocks of all super tiles of one KV head
+    int head;          // length of one KV head's super tiles on the line, in blocks or in pieces
     int end;           // blocks of all sequences up to and including this one (the host keeps T below 2^31)
 };
 
@@ -86,6 +87,10 @@ __host__ __device__ inline long long prefix_blocks(const SeqInfo& s, const Parti
     return up - (k > r ? floor_sum(k - r, KB, T, s.pos0 + r * T - w + 1) : 0);
 }
 
+// Blocks by which a CTA may take longer with whole units than with cut ones: the
+// join costs about as much (2 us against 1 us a block).
+constexpr int kWholeSlack = 2;
+
 __device__ __forceinline__ int warp_inclusive(int v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -96,7 +101,9 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
 }
 
 // Lane's sequence of the 32 starting at base; .end = `before` + inclusive prefix.
-__device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partition& p, int base, int before, int lane) {
+// cut > 0: the line counts pieces of `cut` blocks of each unit, else blocks.
+__device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partition& p, int base, int before, int lane,
+                                              int cut) {
     SeqInfo s{};
     s.b = base + lane;
     if (s.b < c.B) {
@@ -114,7 +121,10 @@ __device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partitio
             visible(s.pos0 + s.n - 1, s.len, p.causal, p.window, x, hi);
             s.lo &= ~(p.align - 1);
             s.blocks = max(1, (hi - s.lo + p.KB - 1) / p.KB);  // no key: one block that writes zeros
-            s.head = s.regular ? static_cast<int>(prefix_blocks(s, p, s.tiles)) : s.tiles * s.blocks;
+            if (cut > 0)
+                s.head = s.tiles * ((s.blocks + cut - 1) / cut);
+            else
+                s.head = s.regular ? static_cast<int>(prefix_blocks(s, p, s.tiles)) : s.tiles * s.blocks;
         }
     }
     s.end = before + warp_inclusive(s.head * c.Hkv, lane);
@@ -138,6 +148,12 @@ __device__ __forceinline__ SeqInfo pick(const SeqInfo& s, int src) {
     return r;
 }
 
+// First key of a regular sequence's super tile k, where its blocks start.
+__device__ __forceinline__ int first_key(const SeqInfo& s, const Partition& p, int k) {
+    const int p0 = s.pos0 + k * (p.R / p.G * p.TS);
+    return p.window > 0 && p0 >= p.window ? (p0 - p.window + 1) & ~(p.KB - 1) : 0;
+}
+
 // A piece of a unit, as one member of the team sees it.
 struct Piece {
     int end;             // no piece: the walk is over
@@ -157,29 +173,56 @@ struct Piece {
 struct Walk {
     SeqInfo mine;  // this lane's sequence of the current chunk
     int base;      // first sequence of the chunk
-    int member;
+    int member, cut;  // cut > 0: the line is made of pieces of `cut` blocks, which no unit shares
     int total, per, t, t_end;
 
     __device__ __forceinline__ void start(const CacheView& c, const Partition& p, int lane, int min_blocks, int cta,
                                           int n_ctas) {
-        int before = 0;
-        for (base = 0;; base += 32) {
-            mine = load_chunk(c, p, base, before, lane);
-            before = __shfl_sync(0xffffffffu, mine.end, 31);
-            if (base + 32 >= c.B) break;
-        }
         const int teams = n_ctas / p.TS;
         member = cta % p.TS;
+        int before = 0, units = 0, most = 0, nominal = 0;  // most: blocks of the longest unit, at most
+        for (base = 0;; base += 32) {
+            mine = load_chunk(c, p, base, before, lane, 0);
+            before = __shfl_sync(0xffffffffu, mine.end, 31);
+            units += __reduce_add_sync(0xffffffffu, mine.tiles);
+            nominal += __reduce_add_sync(0xffffffffu, mine.tiles * mine.blocks);
+            most = max(most, __reduce_max_sync(0xffffffffu, mine.blocks));
+            if (base + 32 >= c.B) break;
+        }
+        units *= c.Hkv;
+        nominal *= c.Hkv;
         total = before;
         per = (total + teams - 1) / teams;
-        if (per < min_blocks) per = min_blocks;
+        cut = 0;
+        if (2 * units <= teams) {
+            // fewer units than teams: each cut by itself, one piece a team.  Even lengths take all teams' share,
+            // others pieces of T / (teams - units), of which there are at most T / that + units = teams.
+            cut = nominal == units * most ? (most + teams / units - 1) / (teams / units)
+                                          : (nominal + teams - units - 1) / (teams - units);
+            if (cut < min_blocks) cut = min_blocks;
+            if (most <= cut + kWholeSlack) cut = most;
+        } else if (static_cast<long long>((units + teams - 1) / teams) * most <= per + kWholeSlack) {
+            cut = most;  // whole units
+        }
+        if (cut > 0) {
+            before = 0;
+            for (base = 0;; base += 32) {
+                mine = load_chunk(c, p, base, before, lane, cut);
+                before = __shfl_sync(0xffffffffu, mine.end, 31);
+                if (base + 32 >= c.B) break;
+            }
+            total = before;
+            per = (total + teams - 1) / teams;
+        } else if (per < min_blocks) {
+            per = min_blocks;
+        }
         // (per * team can pass 2^31 only behind the line's end)
         const long long at = static_cast<long long>(per) * (cta / p.TS);
         t = at < total ? static_cast<int>(at) : total;
         t_end = per < total - t ? t + per : total;
         if (base > 0) {
             base = 0;
-            mine = load_chunk(c, p, 0, 0, lane);
+            mine = load_chunk(c, p, 0, 0, lane, cut);
         }
     }
     // The unit at t and this team's blocks of it; false when the piece is done.
@@ -188,7 +231,7 @@ struct Walk {
         int chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
         while (t >= chunk_end) {
             base += 32;
-            mine = load_chunk(c, p, base, chunk_end, lane);
+            mine = load_chunk(c, p, base, chunk_end, lane, cut);
             chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
         }
         const int src = __ffs(__ballot_sync(0xffffffffu, t < mine.end)) - 1;
@@ -197,12 +240,17 @@ struct Walk {
         q.h = (t - seq0) / s.head;
         const int head0 = seq0 + q.h * s.head, x = t - head0;
         // the super tile: the last k with prefix(k) <= x
-        int k, u0, blocks, lo;
-        if (!s.regular) {
-            k = x / s.blocks;
-            u0 = head0 + k * s.blocks;
+        int k, u0, blocks, lo, len;  // len: the unit's length on the line
+        if (cut > 0 || !s.regular) {
+            len = cut > 0 ? (s.blocks + cut - 1) / cut : s.blocks;
+            k = x / len;
+            u0 = head0 + k * len;
             blocks = s.blocks;
             lo = s.lo;
+            if (s.regular) {
+                blocks = static_cast<int>(prefix_blocks(s, p, k + 1) - prefix_blocks(s, p, k));
+                lo = first_key(s, p, k);
+            }
         } else {
             int from = 0, to = s.tiles;  // prefix(from) <= x < prefix(to)
             while (to - from > 1) {
@@ -215,12 +263,19 @@ struct Walk {
             k = from;
             const int before = static_cast<int>(prefix_blocks(s, p, k));
             u0 = head0 + before;
-            blocks = static_cast<int>(prefix_blocks(s, p, k + 1) - before);
-            const int p0 = s.pos0 + k * (p.R / p.G * p.TS);
-            lo = p.window > 0 && p0 >= p.window ? (p0 - p.window + 1) & ~(p.KB - 1) : 0;
+            len = blocks = static_cast<int>(prefix_blocks(s, p, k + 1) - before);
+            lo = first_key(s, p, k);
         }
-        const int b0 = t - u0, b1 = min(t_end - u0, blocks);
-        t = u0 + b1;
+        int b0, b1;
+        if (cut > 0) {
+            b0 = min((t - u0) * cut, blocks);
+            b1 = min(b0 + cut, blocks);
+            ++t;
+        } else {
+            b0 = t - u0;
+            b1 = min(t_end - u0, blocks);
+            t = u0 + b1;
+        }
         q.end = 0;
         q.b = s.b;
         q.first = s.first;
@@ -228,10 +283,10 @@ struct Walk {
         q.len = s.len;
         q.row0 = (k * p.TS + member) * p.R;
         q.rows = min(p.R, s.n * p.G - q.row0);
-        q.whole = b0 == 0 && b1 == blocks;
-        q.starts = b0 == 0;
         q.t_first = u0 / per;
-        q.t_last = (u0 + blocks - 1) / per;
+        q.t_last = cut > 0 && len == 1 ? q.t_first : (u0 + len - 1) / per;
+        q.whole = cut > 0 ? len == 1 : b0 == 0 && b1 == blocks;
+        q.starts = cut > 0 ? t - 1 == u0 : b0 == 0;
         q.n = 0;
         q.hi = 0;
         q.key0 = lo;

@@ -527,8 +527,8 @@ int dgen_paged_append(const dgen_paged_cache* cache, int32_t n_tokens, const int
  * fp32 receives the natural log of the softmax's sum (-inf for such a row), with
  * which results over parts of a context can be joined.  Scores, softmax and sums
  * are fp32; the weights P enter the second product in about 16 bits (up to 32
- * query rows per KV head and for E4M3 caches) or rounded once to the row type; the
- * output is rounded once.  Cached values
+ * query rows per KV head), in fp16 (bf16 rows over an E4M3 cache) or rounded once to
+ * the row type; the output is rounded once.  Cached values
  * inside a sequence are taken to be finite; nothing behind its end is used.
  * workspace: 16-byte aligned device memory of dgen_paged_workspace_bytes(),
  * zeroed once before its first use (each call leaves its counters at zero);

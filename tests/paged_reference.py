@@ -96,11 +96,15 @@ def attention(cache, q, new, *, scale=None, causal=True, window=0, cap=0.0):
             lse[rows, h] = torch.where(live, top + torch.log(tot), -math.inf)
             if j.numel():
                 worst = torch.where(see, ds, 0.0).amax(1)
-                # weights off by e^ds, the sum likewise; P in 16-bit halves (2^-16), or rounded once to the row
-                # type for more than 32 rows per KV head on a 16-bit cache; fp32 sums over the keys; fp16
-                # weights at worst 2^-25 absolute per key
-                once = n * g > 32 and cache.k_scale is None
-                c = 2 * worst + (torch.finfo(q.dtype).eps / 2 if once else 2.0 ** -16) + (see.sum(1) + 16) * 2.0 ** -24
+                # weights off by e^ds, the sum likewise; P in 16-bit halves (2^-16), or rounded once: to the row
+                # type for more than 32 rows per KV head on a 16-bit cache, to fp16 for bf16 rows on an E4M3
+                # cache; fp32 sums over the keys; fp16 weights at worst 2^-25 absolute per key
+                p_step = 2.0 ** -16
+                if cache.k_scale is None and n * g > 32:
+                    p_step = torch.finfo(q.dtype).eps / 2
+                elif cache.k_scale is not None and q.dtype == torch.bfloat16:
+                    p_step = 2.0 ** -11
+                c = 2 * worst + p_step + (see.sum(1) + 16) * 2.0 ** -24
                 slack[rows, h] = (pr @ vh.abs()) * c[:, None]
                 slack[rows, h] += (see.sum(1) * 2.0 ** -24)[:, None] * vh.abs().amax()
     return out, lse, slack
