@@ -81,6 +81,12 @@ paged::CacheView view(const dgen_paged_cache* c, int n_tokens, const int32_t* cu
     v.table_pages = c->table_pages;
     v.n_tokens = n_tokens;
     v.n_uniform = n_tokens / c->batch;
+    // k = 30 + ceil(log2 page), mul = ceil(2^k / page): mul page - 2^k < page, so pos (mul page - 2^k) < 2^k and
+    // the quotient is exact for every pos < 2^30
+    int bits = 0;
+    while ((int64_t{1} << bits) < c->page_size) ++bits;
+    v.page_shift = 30 + bits;
+    v.page_mul = static_cast<uint32_t>(((uint64_t{1} << v.page_shift) + c->page_size - 1) / c->page_size);
     return v;
 }
 

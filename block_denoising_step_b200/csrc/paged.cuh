@@ -27,6 +27,11 @@ struct CacheView {
     const int* cu;  // [B + 1] first token row of each sequence, or null: n_uniform rows each
     int n_pages, Hkv, page, B, table_stride, table_pages;
     int n_tokens, n_uniform;
+    uint32_t page_mul, page_shift;  // pos / page = pos * page_mul >> page_shift for pos < 2^30
+
+    __device__ __forceinline__ int page_of(int pos) const {
+        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(pos)) * page_mul >> page_shift);
+    }
 };
 
 struct RowsView {  // [tokens][heads][hd], strides in elements
@@ -63,6 +68,12 @@ __device__ __forceinline__ void visible(int p, int len, int causal, int window, 
     lo = window > 0 && p >= window ? p - window + 1 : 0;
     hi = causal ? min(len, p + 1) : (window > 0 && window < len - p ? p + window : len);
     hi = max(hi, lo);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <bool BF>

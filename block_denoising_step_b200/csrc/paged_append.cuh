@@ -76,8 +76,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
             seq_tokens(a.c, b, first, n);
             if (tok - first < n) pos = max(__ldg(a.c.kv_len + b), 0) - n + (tok - first);
             if (pos >= 0) {
-                id = page_entry(a.c, b, pos / a.c.page);
-                off = pos % a.c.page;
+                const int pg = pos < (1 << 30) ? a.c.page_of(pos) : a.c.table_pages;  // (the table ends at 2^30)
+                id = page_entry(a.c, b, pg);
+                off = pos - pg * a.c.page;
             }
         }
         if (lane == 0) {

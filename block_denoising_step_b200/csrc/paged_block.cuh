@@ -89,11 +89,6 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
     return r != 0;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // 32 lanes x 16 consecutive fp32 columns from registers
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -195,10 +190,10 @@ struct Parts {
     int key, id;
     __device__ __forceinline__ void ahead(const CacheView& c, int b, int key_, int hi, int nbox, int lane) {
         key = key_;
-        id = lane < nbox && key < hi ? page_entry(c, b, key / c.page) : -1;
+        id = lane < nbox && key < hi ? page_entry(c, b, c.page_of(key)) : -1;
     }
     __device__ __forceinline__ uint32_t row(const CacheView& c, int h) const {
-        return id >= 0 ? row_in_page(c, id, h, key % c.page) : kNoRow;
+        return id >= 0 ? row_in_page(c, id, h, key - c.page_of(key) * c.page) : kNoRow;
     }
 };
 
@@ -285,7 +280,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             const bool have = walk.next(c, a.p, lane, q);
             q.end = !have;
             if (have && q.n > 0) {  // is a page of its keys absent?
-                const int p0 = q.key0 / c.page, p1 = (min(q.key0 + q.n * kBlkKeys, q.hi) - 1) / c.page;
+                const int p0 = c.page_of(q.key0), p1 = c.page_of(min(q.key0 + q.n * kBlkKeys, q.hi) - 1);
                 bool bad = false;
 #pragma unroll 4
                 for (int e = p0 + lane; e <= p1; e += 32)
@@ -539,7 +534,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 if (s.absent) {  // which page parts are there
                     const int key = k0 + lane * br;
                     have = __ballot_sync(0xffffffffu, lane < nbox && key < s.hi &&
-                                                          static_cast<uint32_t>(page_entry(c, s.b, key / c.page)) <
+                                                          static_cast<uint32_t>(page_entry(c, s.b, c.page_of(key))) <
                                                               static_cast<uint32_t>(c.n_pages));
                 }
                 const uint32_t tb = t_s + buf * kBlkKeys + lane_off;

@@ -39,14 +39,14 @@ struct SplitLayout {
     static constexpr int ROWB = HD * ES;        // bytes of a cache row
     static constexpr int CH = ROWB / 16;        // 16-byte chunks of a row
     // 16-key steps per warp tile
-    static constexpr int MT = NT == 1 && ROWB == 64 ? 2 : 1;
+    static constexpr int MT = NT == 1 && ROWB <= 128 ? 2 : 1;
     // CTAs per SM: short rows need more warps than long ones to keep as many bytes in flight, and a tile's chain
     // of dependent steps (scores, maximum, weights, products) overlapped
-    static constexpr int CTAS = ROWB <= 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : ROWB == 256 ? 2 : 1;
+    static constexpr int CTAS = ROWB <= 128 ? (NT == 4 ? 2 : 3) : ROWB == 256 ? 2 : 1;
     static constexpr int KEYS = 16 * MT;                      // keys per warp tile
     static constexpr int BLOCK_KEYS = kSplitWarps * KEYS;     // keys per block of the line
     static constexpr int TILE = KEYS * ROWB;
-    static constexpr int STAGES = 3;
+    static constexpr int STAGES = NT == 1 && ROWB == 128 ? 2 : 3;
     static constexpr int RING = kSplitWarps * STAGES * 2 * TILE;
 };
 template <int HD, int ES, int NT>
@@ -145,25 +145,28 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
     };
 
     // Fetching: rows of this warp's next tile; the table entry is loaded one tile ahead.
-    int key_next = 0, id_next = -1;
+    int key_next = 0, pg_next = 0, id_next = -1;
+    const uint8_t *k_lane = c.k + lane % CH * 16, *v_lane = c.v + lane % CH * 16;
+    static_assert(CH <= 32 && 32 % CH == 0, "a lane copies the same chunk of every row");
     auto fetch = [&](const Piece& p, int stage, bool live) {
         uint32_t row = kNoRow;
-        if (live && key_next < p.hi) row = row_in_page(c, id_next, p.h, key_next % c.page);
+        if (live && key_next < p.hi) row = row_in_page(c, id_next, p.h, key_next - pg_next * c.page);
         key_next += L::BLOCK_KEYS;
-        id_next = live && key_next < p.hi ? page_entry(c, p.b, key_next / c.page) : -1;
+        pg_next = c.page_of(key_next);
+        id_next = live && key_next < p.hi ? page_entry(c, p.b, pg_next) : -1;
         const uint32_t mask = __ballot_sync(0xffffffffu, row != kNoRow) & kAllKeys;
         if (lane == 0) s_mask[stage] = mask;
         if (mask != 0) {
             const uint32_t dk = ring + stage * (2 * L::TILE), dv = dk + L::TILE;
 #pragma unroll
             for (int i = 0; i < KEYS * CH / 32; ++i) {
-                const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                const int r = i * (32 / CH) + lane / CH;
                 const uint32_t src = __shfl_sync(0xffffffffu, row, r);
                 const bool ok = src != kNoRow;
-                const size_t off = ok ? static_cast<size_t>(src) * L::ROWB + ch * 16 : 0;
-                const uint32_t d = r * L::ROWB + swz_chunk<CH>(r, ch) * 16;
-                attn::cp_async16(dk + d, c.k + off, ok);
-                attn::cp_async16(dv + d, c.v + off, ok);
+                const uint64_t off = static_cast<uint64_t>(ok ? src : 0u) * L::ROWB;
+                const uint32_t d = r * L::ROWB + swz_chunk<CH>(r, lane % CH) * 16;
+                attn::cp_async16(dk + d, k_lane + off, ok);
+                attn::cp_async16(dv + d, v_lane + off, ok);
             }
         }
         attn::cp_commit();
@@ -171,7 +174,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
     // The first tiles of a piece, and its queries into Q buffer i, one warp per row.
     auto begin = [&](const Piece& p, int i) {
         key_next = p.key0 + warp * KEYS + (lane & (KEYS - 1));
-        id_next = key_next < p.hi ? page_entry(c, p.b, key_next / c.page) : -1;
+        pg_next = c.page_of(key_next);
+        id_next = key_next < p.hi ? page_entry(c, p.b, pg_next) : -1;
 #pragma unroll
         for (int e = 0; e < ST - 1; ++e) fetch(p, e, e < p.n);
         float* qscale = reinterpret_cast<float*>(smem + S::QS_OFF) + i * R;
@@ -274,6 +278,15 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
             }
         const float inv_cap = a.cap > 0.f ? kLn2 / a.cap : 0.f;  // of a log2-domain score
 
+        // one tile of rows: its queries' operands stay in registers
+        uint32_t qf[NT == 1 ? HD / 32 : 1][4];
+        if constexpr (NT == 1) {
+#pragma unroll
+            for (int kk = 0; kk < HD / 32; ++kk)
+                attn::ldsm_x4(sq + (lane & 7) * (HD * 2) + swz_chunk<QCH>(lane & 7, 4 * kk + (lane >> 3)) * 16, qf[kk][0],
+                              qf[kk][1], qf[kk][2], qf[kk][3]);
+        }
+
         float o[HD / 16][NT][4];
         float m_run[NT][2], l_run[NT][2];
 #pragma unroll
@@ -307,6 +320,11 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
                     uint32_t b[NT][4];  // k 0-7, 8-15, 16-23, 24-31 of query rows nt * 8 ..
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (NT == 1) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) b[nt][e] = qf[kk][e];
+                            continue;
+                        }
                         const int qr = nt * 8 + (lane & 7);
                         attn::ldsm_x4(sq + qr * (HD * 2) + swz_chunk<QCH>(qr, 4 * kk + (lane >> 3)) * 16, b[nt][0],
                                       b[nt][1], b[nt][2], b[nt][3]);
@@ -411,7 +429,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const float mn = fmaxf(m_run[nt][j], top[nt][j]);
-                            corr[j] = m_run[nt][j] == -INFINITY ? 0.f : exp2f(m_run[nt][j] - mn);
+                            corr[j] = m_run[nt][j] == -INFINITY ? 0.f : ex2(m_run[nt][j] - mn);
                             m_run[nt][j] = mn;
                             l_run[nt][j] *= corr[j];
                         }
@@ -431,7 +449,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
-                            p[e] = exp2f(sc[km][nt][e] - mu);
+                            p[e] = ex2(sc[km][nt][e] - mu);
                             l_run[nt][e & 1] += p[e];
                         }
 #pragma unroll
