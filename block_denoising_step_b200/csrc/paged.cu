@@ -118,6 +118,9 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     using S = paged::SplitSmem<HD, ES, NT>;
     a.p.R = S::R;
     a.p.KB = paged::SplitLayout<HD, ES, NT>::BLOCK_KEYS;
+    a.p.log2_kb = a.p.KB == 64 ? 6 : 7;
+    static_assert(paged::SplitLayout<HD, ES, NT>::BLOCK_KEYS == 64 || paged::SplitLayout<HD, ES, NT>::BLOCK_KEYS == 128,
+                  "log2_kb");
     a.p.align = rows_most <= S::R ? 1 : a.p.KB;
     a.p.TS = 1;
     auto kern = paged::paged_split_kernel<HD, ES, BF, NT>;
@@ -192,6 +195,7 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     const int tokens = paged::kBlkRows / a.p.G;  // per row tile
     a.p.R = tokens * a.p.G;
     a.p.KB = a.p.align = paged::kBlkKeys;
+    a.p.log2_kb = 7;
     int log2_br = 3;
     while (log2_br < 7 && a.c.page % (2 << log2_br) == 0) ++log2_br;
     CUtensorMap tq, tk, tv;

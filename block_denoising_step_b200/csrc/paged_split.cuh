@@ -307,13 +307,14 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
             const int key0 = key_first + i * L::BLOCK_KEYS;
             if (mask != 0) {  // (warp-uniform)
                 const uint32_t tk = ring + stage * (2 * L::TILE), tv = tk + L::TILE;
-                float sc[MT][NT][4];
+                // (two accumulators each: products on one wait for each other)
+                float sc[MT][NT][4], sd[MT][NT][4];
 #pragma unroll
                 for (int km = 0; km < MT; ++km)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[km][nt][e] = 0.f;
+                        for (int e = 0; e < 4; ++e) sc[km][nt][e] = sd[km][nt][e] = 0.f;
                 // S^T = K Q^T, 32 elements of hd per step
 #pragma unroll
                 for (int kk = 0; kk < HD / 32; ++kk) {
@@ -354,10 +355,16 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_16816<BF>(sc[km][nt], ka[0], b[nt][0], b[nt][1]);
-                            mma_16816<BF>(sc[km][nt], ka[1], b[nt][2], b[nt][3]);
+                            mma_16816<BF>(sd[km][nt], ka[1], b[nt][2], b[nt][3]);
                         }
                     }
                 }
+#pragma unroll
+                for (int km = 0; km < MT; ++km)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[km][nt][e] += sd[km][nt][e];
                 // log2-domain scores, masks, running maximum
                 if (a.cap > 0.f) {
                     bool small = true;
@@ -460,45 +467,47 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
                             if (low) pl[km][nt][half] = movmatrix_t(H2::pack(p[2 * half] - hf.x, p[2 * half + 1] - hf.y));
                         }
                     }
-                // O^T += V^T P^T
+                // O^T += V^T P^T, four (two) rows of tiles at a time, all their hi parts before the lo parts
                 const int vc = (lane >> 3) & 1;
+                constexpr int GM = HD == 256 || NT > 1 ? 2 : 4;
 #pragma unroll
                 for (int km = 0; km < MT; ++km) {
                     const int vr = km * 16 + (lane & 7) + ((lane >> 4) << 3);
-                    if constexpr (ES == 2) {
 #pragma unroll
-                        for (int mt = 0; mt < HD / 16; ++mt) {
-                            uint32_t va[4];
-                            attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mt + vc) * 16, va[0], va[1],
-                                            va[2], va[3]);
+                    for (int m0 = 0; m0 < HD / 16; m0 += GM) {
+                        uint32_t va[GM][4];
+                        if constexpr (ES == 2) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma_16816<BF>(o[mt][nt], va, ph[km][nt][0], ph[km][nt][1]);
-                                mma_16816<BF>(o[mt][nt], va, pl[km][nt][0], pl[km][nt][1]);
+                            for (int i = 0; i < GM; ++i)
+                                attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * (m0 + i) + vc) * 16, va[i][0],
+                                                va[i][1], va[i][2], va[i][3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < GM; i += 2) {
+                                uint32_t x[4];  // two 16-byte columns x keys 0-7, then keys 8-15
+                                attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, m0 + i + vc) * 16, x[0], x[1],
+                                                x[2], x[3]);
+#pragma unroll
+                                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        // bytes 2g, 2g + 1 of key 2t, then of key 2t + 1: rows g and g + 8
+                                        const uint32_t v = __byte_perm(x[2 * half + u], 0, 0x3120);
+                                        va[i + u][2 * half] = e4m3x2_f16x2(static_cast<uint16_t>(v));
+                                        va[i + u][2 * half + 1] = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
+                                    }
                             }
                         }
-                    } else {
 #pragma unroll
-                        for (int mp = 0; mp < HD / 32; ++mp) {
-                            uint32_t x[4];  // two 16-byte columns x keys 0-7, then keys 8-15
-                            attn::ldsm_x4_t(tv + vr * L::ROWB + swz_chunk<CH>(vr, 2 * mp + vc) * 16, x[0], x[1], x[2],
-                                            x[3]);
+                        for (int i = 0; i < GM; ++i)
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                uint32_t va[4];
+                            for (int nt = 0; nt < NT; ++nt) mma_16816<BF>(o[m0 + i][nt], va[i], ph[km][nt][0], ph[km][nt][1]);
+                        if (low) {
 #pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    // bytes 2g, 2g + 1 of key 2t, then of key 2t + 1: rows g and g + 8
-                                    const uint32_t v = __byte_perm(x[2 * half + u], 0, 0x3120);
-                                    va[2 * half] = e4m3x2_f16x2(static_cast<uint16_t>(v));
-                                    va[2 * half + 1] = e4m3x2_f16x2(static_cast<uint16_t>(v >> 16));
-                                }
+                            for (int i = 0; i < GM; ++i)
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    mma_16816<BF>(o[2 * mp + u][nt], va, ph[km][nt][0], ph[km][nt][1]);
-                                    if (low) mma_16816<BF>(o[2 * mp + u][nt], va, pl[km][nt][0], pl[km][nt][1]);
-                                }
-                            }
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_16816<BF>(o[m0 + i][nt], va[i], pl[km][nt][0], pl[km][nt][1]);
                         }
                     }
                 }

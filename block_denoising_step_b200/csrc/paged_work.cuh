@@ -38,7 +38,7 @@ struct SeqInfo {
 };
 
 struct Partition {
-    int G, R, TS, KB, causal, window;
+    int G, R, TS, KB, log2_kb, causal, window;
     int align;               // blocks start at multiples of it: KB, or 1 where sequences have one tile
     int rows_min, rows_max;  // query rows per KV head of the sequences this launch takes
 };
@@ -100,35 +100,37 @@ __device__ __forceinline__ int warp_inclusive(int v, int lane) {
     return v;
 }
 
-// Lane's sequence of the 32 starting at base; .end = `before` + inclusive prefix.
-// cut > 0: the line counts pieces of `cut` blocks of each unit, else blocks.
-__device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partition& p, int base, int before, int lane,
-                                              int cut) {
+// Lane's sequence of the 32 starting at base.
+__device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partition& p, int base, int lane) {
     SeqInfo s{};
     s.b = base + lane;
     if (s.b < c.B) {
-        seq_tokens(c, s.b, s.first, s.n);
         const int full = max(__ldg(c.kv_len + s.b), 0);
+        seq_tokens(c, s.b, s.first, s.n);
         s.pos0 = full - s.n;
         const long long cap = static_cast<long long>(c.table_pages) * c.page;
         s.len = full < cap ? full : static_cast<int>(cap);
         const int rows = s.n * p.G;
         if (rows >= p.rows_min && rows <= p.rows_max && rows > 0) {
-            s.tiles = (rows + p.R * p.TS - 1) / (p.R * p.TS);
+            s.tiles = rows <= p.R * p.TS ? 1 : (rows + p.R * p.TS - 1) / (p.R * p.TS);
             s.regular = s.tiles > 1 && p.align == p.KB && s.pos0 >= 0 && s.len == full;
             int hi, x;
             visible(s.pos0, s.len, p.causal, p.window, s.lo, x);
             visible(s.pos0 + s.n - 1, s.len, p.causal, p.window, x, hi);
             s.lo &= ~(p.align - 1);
-            s.blocks = max(1, (hi - s.lo + p.KB - 1) / p.KB);  // no key: one block that writes zeros
-            if (cut > 0)
-                s.head = s.tiles * ((s.blocks + cut - 1) / cut);
-            else
-                s.head = s.regular ? static_cast<int>(prefix_blocks(s, p, s.tiles)) : s.tiles * s.blocks;
+            s.blocks = max(1, (hi - s.lo + p.KB - 1) >> p.log2_kb);  // no key: one block that writes zeros
         }
     }
-    s.end = before + warp_inclusive(s.head * c.Hkv, lane);
     return s;
+}
+// Its length on the line, and the line's up to it (`before` the chunk).  cut > 0:
+// the line counts pieces of `cut` blocks of each unit, else blocks.
+__device__ __forceinline__ void place(SeqInfo& s, const CacheView& c, const Partition& p, int cut, int before, int lane) {
+    if (cut > 0)
+        s.head = s.tiles * (s.blocks <= cut ? 1 : (s.blocks + cut - 1) / cut);
+    else
+        s.head = s.regular ? static_cast<int>(prefix_blocks(s, p, s.tiles)) : s.tiles * s.blocks;
+    s.end = before + warp_inclusive(s.head * c.Hkv, lane);
 }
 
 __device__ __forceinline__ SeqInfo pick(const SeqInfo& s, int src) {
@@ -178,11 +180,12 @@ struct Walk {
 
     __device__ __forceinline__ void start(const CacheView& c, const Partition& p, int lane, int min_blocks, int cta,
                                           int n_ctas) {
-        const int teams = n_ctas / p.TS;
-        member = cta % p.TS;
+        const int log2_ts = __ffs(p.TS) - 1, teams = n_ctas >> log2_ts;  // (TS is a power of two)
+        member = cta & (p.TS - 1);
         int before = 0, units = 0, most = 0, nominal = 0;  // most: blocks of the longest unit, at most
         for (base = 0;; base += 32) {
-            mine = load_chunk(c, p, base, before, lane, 0);
+            mine = load_chunk(c, p, base, lane);
+            place(mine, c, p, 0, before, lane);
             before = __shfl_sync(0xffffffffu, mine.end, 31);
             units += __reduce_add_sync(0xffffffffu, mine.tiles);
             nominal += __reduce_add_sync(0xffffffffu, mine.tiles * mine.blocks);
@@ -207,7 +210,8 @@ struct Walk {
         if (cut > 0) {
             before = 0;
             for (base = 0;; base += 32) {
-                mine = load_chunk(c, p, base, before, lane, cut);
+                if (c.B > 32) mine = load_chunk(c, p, base, lane);
+                place(mine, c, p, cut, before, lane);
                 before = __shfl_sync(0xffffffffu, mine.end, 31);
                 if (base + 32 >= c.B) break;
             }
@@ -217,12 +221,13 @@ struct Walk {
             per = min_blocks;
         }
         // (per * team can pass 2^31 only behind the line's end)
-        const long long at = static_cast<long long>(per) * (cta / p.TS);
+        const long long at = static_cast<long long>(per) * (cta >> log2_ts);
         t = at < total ? static_cast<int>(at) : total;
         t_end = per < total - t ? t + per : total;
         if (base > 0) {
             base = 0;
-            mine = load_chunk(c, p, 0, 0, lane, cut);
+            mine = load_chunk(c, p, 0, lane);
+            place(mine, c, p, cut, 0, lane);
         }
     }
     // The unit at t and this team's blocks of it; false when the piece is done.
@@ -231,7 +236,8 @@ struct Walk {
         int chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
         while (t >= chunk_end) {
             base += 32;
-            mine = load_chunk(c, p, base, chunk_end, lane, cut);
+            mine = load_chunk(c, p, base, lane);
+            place(mine, c, p, cut, chunk_end, lane);
             chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
         }
         const int src = __ffs(__ballot_sync(0xffffffffu, t < mine.end)) - 1;
@@ -242,8 +248,8 @@ struct Walk {
         // the super tile: the last k with prefix(k) <= x
         int k, u0, blocks, lo, len;  // len: the unit's length on the line
         if (cut > 0 || !s.regular) {
-            len = cut > 0 ? (s.blocks + cut - 1) / cut : s.blocks;
-            k = x / len;
+            len = cut <= 0 ? s.blocks : s.blocks <= cut ? 1 : (s.blocks + cut - 1) / cut;
+            k = s.tiles == 1 ? 0 : x / len;
             u0 = head0 + k * len;
             blocks = s.blocks;
             lo = s.lo;
@@ -283,8 +289,8 @@ struct Walk {
         q.len = s.len;
         q.row0 = (k * p.TS + member) * p.R;
         q.rows = min(p.R, s.n * p.G - q.row0);
-        q.t_first = u0 / per;
-        q.t_last = cut > 0 && len == 1 ? q.t_first : (u0 + len - 1) / per;
+        q.t_first = per == 1 ? u0 : u0 / per;
+        q.t_last = cut > 0 && len == 1 ? q.t_first : per == 1 ? u0 + len - 1 : (u0 + len - 1) / per;
         q.whole = cut > 0 ? len == 1 : b0 == 0 && b1 == blocks;
         q.starts = cut > 0 ? t - 1 == u0 : b0 == 0;
         q.n = 0;
@@ -295,7 +301,7 @@ struct Walk {
             visible(s.pos0 + q.row0 / p.G, s.len, p.causal, p.window, my_lo, x0);
             visible(s.pos0 + (q.row0 + q.rows - 1) / p.G, s.len, p.causal, p.window, x0, q.hi);
             if (q.hi > my_lo) {
-                const int j0 = max(b0, (my_lo - lo) / p.KB), j1 = min(b1, (q.hi - lo + p.KB - 1) / p.KB);
+                const int j0 = max(b0, (my_lo - lo) >> p.log2_kb), j1 = min(b1, (q.hi - lo + p.KB - 1) >> p.log2_kb);
                 q.n = max(0, j1 - j0);
                 q.key0 = lo + j0 * p.KB;
             }
