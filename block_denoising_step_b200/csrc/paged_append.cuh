@@ -7,15 +7,16 @@
 // go to their page (bf16 / fp16, or x / scale[head] as E4M3), rotated queries to
 // q_out.  The rotation is computed in fp32 and rounded once.
 //
-// The angle is taken in double as turns, t = pos * (base^(-2j/hd) / 2 pi), of
-// which only the fraction enters the fp32 sine and cosine: positions in the
-// millions keep 1e-7 of absolute accuracy without a table.  Each block computes
-// the hd/2 frequencies once and its tokens' sines once, for all heads.
+// The angle is taken in double as turns, t = pos * (base^(-2j/hd) / 2 pi), and so are
+// the sine and cosine of its fraction, rounded to fp32 once: positions in the
+// millions are as exact as small ones, without a table.  A block computes the hd/2
+// frequencies once and its tokens' sines once, for all heads.
 //
 // Memory-bound: every row is read and written once, 16 bytes per access.  A
 // block takes up to kTokens tokens (one warp each finds its token's sequence
-// and page), then all threads sweep (row, 8 + 8 elements) items, kUnroll loads
-// in flight each.
+// and page), then all threads sweep (row, 8 + 8 elements) items.  A thread's next
+// items are on their way while it writes the current ones, the first ones already
+// while the pages are looked up, which their addresses do not need.
 #pragma once
 
 #include "paged.cuh"
@@ -52,10 +53,19 @@ __device__ __forceinline__ int find_sequence(const CacheView& c, int tok, int la
     return b < c.B ? b : -1;
 }
 
+// x / s for E4M3: x times 1 / s, corrected by the remainder (as a division is, without
+// its special cases; an infinite quotient stays).  inv = 1 / s, s and 1 / s normal.
+__device__ __forceinline__ float scaled_down(float x, float s, float inv) {
+    const float q = x * inv, r = fmaf(fmaf(-q, s, x), inv, q);
+    return r == r ? r : q;
+}
+
 template <int HD, bool BF, bool E4M3>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a, int tokens_per_block) {
+__global__ void __launch_bounds__(kAppendThreads, E4M3 ? 3 : 4) paged_append_kernel(const AppendArgs a, int tokens_per_block) {
     constexpr int HALF = HD / 2;
     constexpr int CH = HALF / 8;  // items per row: 8 elements of each half
+    constexpr int STEP = kAppendThreads / CH;  // rows between a thread's items
+    constexpr int U = 2;                       // items in flight besides the ones at hand
     __shared__ double freq[HALF];
     __shared__ float2 cs[kAppendTokens][HALF];
     __shared__ int s_pos[kAppendTokens], s_page[kAppendTokens], s_off[kAppendTokens];
@@ -64,6 +74,31 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tok0 = blockIdx.x * tokens_per_block;
     const int nt = min(tokens_per_block, a.c.n_tokens - tok0);
+    const int rows = a.Hq + 2 * a.c.Hkv, c = threadIdx.x % CH;
+    // the items of this thread: (token t, row), always the same chunk
+    int lt = 0, lrow = threadIdx.x / CH;  // the next item to load
+    auto settle = [&](int& t, int& row) {
+        while (row >= rows) {
+            row -= rows;
+            ++t;
+        }
+    };
+    uint4 lo[U], hi[U];
+    auto load = [&]() {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            settle(lt, lrow);
+            if (lt < nt) {
+                const RowsView& src = lrow < a.Hq ? a.q : (lrow < a.Hq + a.c.Hkv ? a.k : a.v);
+                const int h = lrow < a.Hq ? lrow : lrow - a.Hq - (lrow < a.Hq + a.c.Hkv ? 0 : a.c.Hkv);
+                const uint4* p = reinterpret_cast<const uint4*>(src.p + ((tok0 + lt) * src.ts + h * src.hs + c * 8) * 2);
+                lo[u] = *p;
+                hi[u] = *(p + HALF / 8);
+            }
+            lrow += STEP;
+        }
+    };
+    load();
     if (a.rotate)
         for (int j = threadIdx.x; j < HALF; j += kAppendThreads)
             freq[j] = exp2(-a.log2_base * j / HALF) * 0.15915494309189533577;  // turns per position
@@ -73,8 +108,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
         int pos = -1, id = -1, off = 0;
         if (b >= 0) {
             int first, n;
+            const int len = max(__ldg(a.c.kv_len + b), 0);
             seq_tokens(a.c, b, first, n);
-            if (tok - first < n) pos = max(__ldg(a.c.kv_len + b), 0) - n + (tok - first);
+            if (tok - first < n) pos = len - n + (tok - first);
             if (pos >= 0) {
                 const int pg = pos < (1 << 30) ? a.c.page_of(pos) : a.c.table_pages;  // (the table ends at 2^30)
                 id = page_entry(a.c, b, pg);
@@ -92,83 +128,96 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
         for (int i = threadIdx.x; i < nt * HALF; i += kAppendThreads) {
             const int t = i / HALF, j = i % HALF;
             const double turns = freq[j] * s_pos[t];
-            float s, co;
-            sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &co);
-            cs[t][j] = make_float2(co, s);
+            double s, co;
+            sincospi(2.0 * (turns - rint(turns)), &s, &co);
+            cs[t][j] = make_float2(static_cast<float>(co), static_cast<float>(s));
         }
         __syncthreads();
     }
-    const int rows = a.Hq + 2 * a.c.Hkv;
-    const int items = nt * rows * CH;
-    constexpr int U = 4;
-    for (int i0 = threadIdx.x; i0 < items; i0 += U * kAppendThreads) {
-        uint4 lo[U], hi[U];
+    int t = 0, row = threadIdx.x / CH;
+    settle(t, row);
+    while (t < nt) {
+        uint4 xl[U], xh[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kAppendThreads;
-            if (i < items) {
-                const int c = i % CH, row = (i / CH) % rows, tok = tok0 + i / (CH * rows);
-                const RowsView& src = row < a.Hq ? a.q : (row < a.Hq + a.c.Hkv ? a.k : a.v);
-                const int h = row < a.Hq ? row : (row - a.Hq) % a.c.Hkv;
-                const uint4* p = reinterpret_cast<const uint4*>(src.p + (tok * src.ts + h * src.hs + c * 8) * 2);
-                lo[u] = *p;
-                hi[u] = *(p + HALF / 8);
-            }
+            xl[u] = lo[u];
+            xh[u] = hi[u];
         }
+        load();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kAppendThreads;
-            if (i >= items) break;
-            const int c = i % CH, row = (i / CH) % rows, t = i / (CH * rows);
-            if (s_pos[t] < 0) continue;
-            const bool is_q = row < a.Hq, is_v = row >= a.Hq + a.c.Hkv;
-            const int h = is_q ? row : (row - a.Hq) % a.c.Hkv;
-            if (!is_q && static_cast<uint32_t>(s_page[t]) >= static_cast<uint32_t>(a.c.n_pages)) continue;
-            uint32_t* L = reinterpret_cast<uint32_t*>(&lo[u]);
-            uint32_t* H = reinterpret_cast<uint32_t*>(&hi[u]);
+            settle(t, row);
+            const int tt = t, rr = row;
+            row += STEP;
+            if (tt >= nt || s_pos[tt] < 0) continue;
+            const bool is_q = rr < a.Hq, is_v = rr >= a.Hq + a.c.Hkv;
+            const int h = is_q ? rr : rr - a.Hq - (is_v ? a.c.Hkv : 0);
+            if (!is_q && static_cast<uint32_t>(s_page[tt]) >= static_cast<uint32_t>(a.c.n_pages)) continue;
+            uint32_t* L = reinterpret_cast<uint32_t*>(&xl[u]);
+            uint32_t* H = reinterpret_cast<uint32_t*>(&xh[u]);
+            const bool turn = a.rotate && !is_v;
             float2 x[4], y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = H2::unpack(L[e]);
-                y[e] = H2::unpack(H[e]);
-            }
-            if (a.rotate && !is_v) {
+            if (turn || (E4M3 && !is_q)) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 c0 = cs[t][c * 8 + 2 * e], c1 = cs[t][c * 8 + 2 * e + 1];
+                    x[e] = H2::unpack(L[e]);
+                    y[e] = H2::unpack(H[e]);
+                }
+            }
+            if (turn) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 w = *reinterpret_cast<const float4*>(&cs[tt][c * 8 + 2 * e]);  // cos, sin, cos, sin
                     const float2 p = x[e], r = y[e];
-                    x[e] = make_float2(p.x * c0.x - r.x * c0.y, p.y * c1.x - r.y * c1.y);
-                    y[e] = make_float2(r.x * c0.x + p.x * c0.y, r.y * c1.x + p.y * c1.y);
+                    x[e] = make_float2(p.x * w.x - r.x * w.y, p.y * w.z - r.y * w.w);
+                    y[e] = make_float2(r.x * w.x + p.x * w.y, r.y * w.z + p.y * w.w);
                 }
             }
             if (E4M3 && !is_q) {
-                const float s = __ldg((is_v ? a.c.v_scale : a.c.k_scale) + h);
+                const float s = __ldg((is_v ? a.c.v_scale : a.c.k_scale) + h), inv = 1.f / s;
                 uint32_t o[4];
+                auto pack4 = [&](float2 p, float2 r) -> uint32_t {
+                    return pack2_e4m3(p.x, p.y) | (static_cast<uint32_t>(pack2_e4m3(r.x, r.y)) << 16);
+                };
+                if (s > 1e-30f && s < 1e30f) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = make_float2(scaled_down(x[e].x, s, inv), scaled_down(x[e].y, s, inv));
+                        y[e] = make_float2(scaled_down(y[e].x, s, inv), scaled_down(y[e].y, s, inv));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = make_float2(x[e].x / s, x[e].y / s);
+                        y[e] = make_float2(y[e].x / s, y[e].y / s);
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    o[e] = pack2_e4m3(x[2 * e].x / s, x[2 * e].y / s) |
-                           (static_cast<uint32_t>(pack2_e4m3(x[2 * e + 1].x / s, x[2 * e + 1].y / s)) << 16);
-                    o[2 + e] = pack2_e4m3(y[2 * e].x / s, y[2 * e].y / s) |
-                               (static_cast<uint32_t>(pack2_e4m3(y[2 * e + 1].x / s, y[2 * e + 1].y / s)) << 16);
+                    o[e] = pack4(x[2 * e], x[2 * e + 1]);
+                    o[2 + e] = pack4(y[2 * e], y[2 * e + 1]);
                 }
                 uint8_t* base = (is_v ? a.c.v : a.c.k) +
-                                static_cast<size_t>(row_in_page(a.c, s_page[t], h, s_off[t])) * HD + c * 8;
+                                static_cast<size_t>(row_in_page(a.c, s_page[tt], h, s_off[tt])) * HD + c * 8;
                 *reinterpret_cast<uint2*>(base) = make_uint2(o[0], o[1]);
                 *reinterpret_cast<uint2*>(base + HALF) = make_uint2(o[2], o[3]);
             } else {
+                if (turn) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    L[e] = H2::pack(x[e].x, x[e].y);
-                    H[e] = H2::pack(y[e].x, y[e].y);
+                    for (int e = 0; e < 4; ++e) {
+                        L[e] = H2::pack(x[e].x, x[e].y);
+                        H[e] = H2::pack(y[e].x, y[e].y);
+                    }
                 }
                 uint8_t* base =
-                    is_q ? a.q_out.p + ((tok0 + t) * a.q_out.ts + h * a.q_out.hs + c * 8) * 2
+                    is_q ? a.q_out.p + ((tok0 + tt) * a.q_out.ts + h * a.q_out.hs + c * 8) * 2
                          : (is_v ? a.c.v : a.c.k) +
-                               (static_cast<size_t>(row_in_page(a.c, s_page[t], h, s_off[t])) * HD + c * 8) * 2;
-                *reinterpret_cast<uint4*>(base) = lo[u];
-                *reinterpret_cast<uint4*>(base + HD) = hi[u];
+                               (static_cast<size_t>(row_in_page(a.c, s_page[tt], h, s_off[tt])) * HD + c * 8) * 2;
+                *reinterpret_cast<uint4*>(base) = xl[u];
+                *reinterpret_cast<uint4*>(base + HD) = xh[u];
             }
         }
+        settle(t, row);
     }
 }
 
