@@ -123,6 +123,7 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
                   "log2_kb");
     a.p.align = rows_most <= S::R ? 1 : a.p.KB;
     a.p.TS = 1;
+    a.p.tokens = S::R / a.p.G;
     auto kern = paged::paged_split_kernel<HD, ES, BF, NT>;
     set_smem_attr_once(kern, S::BYTES, dev);
     static std::atomic<int> per_sm{0};  // resident CTAs per SM: a property of the kernel
@@ -219,6 +220,7 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     a.p.TS = 1;
     for (int ts : {4, 2})
         if (a.p.TS == 1 && (ts == 2 || !a.c.cu) && 8 * avg >= 7 * ((avg + ts - 1) / ts * ts)) a.p.TS = ts;
+    a.p.tokens = tokens * a.p.TS;
     const int64_t units = std::min<int64_t>(rows, rows / (a.p.R * a.p.TS) + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + 2 * paged::kBlkKeys - 2) / paged::kBlkKeys;
     if (units * blocks >= INT32_MAX) return DGEN_EINVAL;

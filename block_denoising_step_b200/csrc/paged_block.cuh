@@ -279,14 +279,6 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             Piece q{};
             const bool have = walk.next(c, a.p, lane, q);
             q.end = !have;
-            if (have && q.n > 0) {  // is a page of its keys absent?
-                const int p0 = c.page_of(q.key0), p1 = c.page_of(min(q.key0 + q.n * kBlkKeys, q.hi) - 1);
-                bool bad = false;
-#pragma unroll 4
-                for (int e = p0 + lane; e <= p1; e += 32)
-                    bad |= static_cast<uint32_t>(page_entry(c, q.b, e)) >= static_cast<uint32_t>(c.n_pages);
-                q.absent = __any_sync(0xffffffffu, bad);
-            }
             // what the join kernel has to know of the unit that starts here and goes on behind
             if (lane == 0 && (!have || (q.starts && !q.whole && q.rows > 0))) {
                 if (have || !cut) a.joins[blockIdx.x] = q;
@@ -523,6 +515,15 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             visible(s.pos0 + (row0 + min(row, rows - 1)) / a.p.G, s.len, a.p.causal, a.p.window, vlo, vhi);
             // keys every row of this warp sees (ranges only move up with the row)
             const int all_lo = __shfl_sync(0xffffffffu, vlo, 31), all_hi = __shfl_sync(0xffffffffu, vhi, 0);
+            // is a page of these keys absent?  (looked up while the first scores are on their way)
+            bool absent = false;
+            if (n > 0) {
+                const int p1 = c.page_of(min(key0 + n * kBlkKeys, s.hi) - 1);
+#pragma unroll 4
+                for (int e = c.page_of(key0) + lane; e <= p1; e += 32)
+                    absent |= static_cast<uint32_t>(page_entry(c, s.b, e)) >= static_cast<uint32_t>(c.n_pages);
+                absent = __any_sync(0xffffffffu, absent);
+            }
             float m_run = -INFINITY, l_run = 0.f;  // the maximum this warp's l is relative to
             // the slots of m are free once every warp has read the sums of the unit before
             if (n > 0 && unit_no > 0 &&
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             for (int j = (jj ^ grp) & 1; ok && j < n; j += 2) {
                 const int t = jj + j, buf = t % NB, k0 = key0 + j * kBlkKeys;
                 uint32_t have = all_parts;
-                if (s.absent) {  // which page parts are there
+                if (absent) {  // which page parts are there
                     const int key = k0 + lane * br;
                     have = __ballot_sync(0xffffffffu, lane < nbox && key < s.hi &&
                                                           static_cast<uint32_t>(page_entry(c, s.b, c.page_of(key))) <
@@ -771,7 +772,7 @@ template <int HD, bool BF>
 __global__ void __launch_bounds__(256) paged_block_join_kernel(const AttendArgs a) {
     using H2 = Half2<BF>;
     pdl_enter();
-    const int cta = blockIdx.x, member = cta % a.p.TS;
+    const int cta = blockIdx.x, member = cta & (a.p.TS - 1);
     const Piece s = a.joins[cta];
     const int row = threadIdx.x & (kBlkRows - 1), col = blockIdx.y * kJoinCols + (threadIdx.x >> 7) * 8;
     if (s.end || row >= s.rows) return;

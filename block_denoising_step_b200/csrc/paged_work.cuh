@@ -39,23 +39,25 @@ struct SeqInfo {
 
 struct Partition {
     int G, R, TS, KB, log2_kb, causal, window;
+    int tokens;              // of a super tile: R / G * TS
     int align;               // blocks start at multiples of it: KB, or 1 where sequences have one tile
     int rows_min, rows_max;  // query rows per KV head of the sequences this launch takes
 };
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid's scheme on the lattice
-// points below the line)
-__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum over i < n of floor((a i + b) / m) (Euclid's scheme on the lattice points
+// below the line); a n + b below 2^31
+__host__ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     long long sum = 0;
     while (n > 0) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const long long y = a * n + b;
+        const uint32_t qa = a / m, qb = b / m;
+        sum += static_cast<long long>(n) * (n - 1) / 2 * qa + static_cast<long long>(n) * qb;
+        a -= qa * m;
+        b -= qb * m;
+        const uint32_t y = a * n + b;
         if (y < m) break;
         n = y / m;
-        b = y % m;
-        const long long t = m;
+        b = y - n * m;
+        const uint32_t t = m;
         m = a;
         a = t;
     }
@@ -64,27 +66,33 @@ __host__ __device__ inline long long floor_sum(long long n, long long m, long lo
 
 // Blocks of the super tiles before number k of a regular sequence (pos0 >= 0,
 // len = pos0 + n): tile i holds the tokens i T .. (T = tokens of a super tile) and
-// sees blocks floor(lo / KB) .. ceil(hi / KB) - 1.
-__host__ __device__ inline long long prefix_blocks(const SeqInfo& s, const Partition& p, int k) {
-    const long long T = p.R / p.G * p.TS, KB = p.KB, n = s.n, w = p.window, whole = (s.len + KB - 1) / KB;
-    long long up;  // sum of ceil(hi / KB)
-    if (p.causal) {
-        const long long m = k < s.tiles ? k : s.tiles - 1;  // the last tile may be short
-        up = floor_sum(m, KB, T, s.pos0 + T + KB - 1) + (k - m) * whole;
-    } else if (w == 0) {
-        up = k * whole;
+// sees blocks floor(lo / KB) .. ceil(hi / KB) - 1.  (Positions are below 2^30, and
+// so is every sum of blocks here: the host bounds the line.)
+// (Not inlined: a launch's first pass over any code waits for it, and this is long.)
+__host__ __device__ __noinline__ static int prefix_masked(int n, int len, int pos0, int tiles, int T, int KB, int whole,
+                                                          int causal, int window, int k) {
+    int up;  // sum of ceil(hi / KB)
+    if (causal) {
+        const int m = k < tiles ? k : tiles - 1;  // the last tile may be short
+        up = static_cast<int>(floor_sum(m, KB, T, pos0 + T + KB - 1)) + (k - m) * whole;
     } else {  // hi = min(len, pos0 + (i + 1) T - 1 + w): reaches len from tile r on
-        long long r = n + 1 - w <= 0 ? 0 : (n + 1 - w + T - 1) / T - 1;
-        if (r < 0) r = 0;
-        if (r > s.tiles - 1) r = s.tiles - 1;
-        const long long m = k < r ? k : r;
-        up = floor_sum(m, KB, T, s.pos0 + T - 1 + w + KB - 1) + (k - m) * whole;
+        const long long d = static_cast<long long>(n) + 1 - window;
+        int r = d <= 0 ? 0 : (static_cast<int>(d) + T - 1) / T - 1;
+        r = r < 0 ? 0 : r > tiles - 1 ? tiles - 1 : r;
+        const int m = k < r ? k : r;
+        up = (m > 0 ? static_cast<int>(floor_sum(m, KB, T, pos0 + T - 1 + window + KB - 1)) : 0) + (k - m) * whole;
     }
-    if (w == 0) return up;
+    if (window == 0) return up;
     // lo = max(0, pos0 + i T - w + 1): positive from tile r on
-    const long long d = w - 1 - s.pos0;
-    const long long r = d <= 0 ? 0 : (d + T - 1) / T;
-    return up - (k > r ? floor_sum(k - r, KB, T, s.pos0 + r * T - w + 1) : 0);
+    const int d = window - 1 - pos0;
+    const int r = d <= 0 ? 0 : d > (1 << 30) ? k : (d + T - 1) / T;
+    return up - (k > r ? static_cast<int>(floor_sum(k - r, KB, T, pos0 + r * T - window + 1)) : 0);
+}
+__host__ __device__ inline int prefix_blocks(const SeqInfo& s, const Partition& p, int k) {
+    const int whole = (s.len + p.KB - 1) >> p.log2_kb;
+    return !p.causal && p.window == 0 ? k * whole
+                                      : prefix_masked(s.n, s.len, s.pos0, s.tiles, p.tokens, p.KB, whole, p.causal,
+                                                      p.window, k);
 }
 
 // Blocks by which a CTA may take longer with whole units than with cut ones: the
@@ -129,7 +137,7 @@ __device__ __forceinline__ void place(SeqInfo& s, const CacheView& c, const Part
     if (cut > 0)
         s.head = s.tiles * (s.blocks <= cut ? 1 : (s.blocks + cut - 1) / cut);
     else
-        s.head = s.regular ? static_cast<int>(prefix_blocks(s, p, s.tiles)) : s.tiles * s.blocks;
+        s.head = s.regular ? prefix_blocks(s, p, s.tiles) : s.tiles * s.blocks;
     s.end = before + warp_inclusive(s.head * c.Hkv, lane);
 }
 
@@ -152,7 +160,7 @@ __device__ __forceinline__ SeqInfo pick(const SeqInfo& s, int src) {
 
 // First key of a regular sequence's super tile k, where its blocks start.
 __device__ __forceinline__ int first_key(const SeqInfo& s, const Partition& p, int k) {
-    const int p0 = s.pos0 + k * (p.R / p.G * p.TS);
+    const int p0 = s.pos0 + k * p.tokens;
     return p.window > 0 && p0 >= p.window ? (p0 - p.window + 1) & ~(p.KB - 1) : 0;
 }
 
@@ -168,7 +176,6 @@ struct Piece {
     int hi;              // keys from here on are not seen by any of its rows
     int whole, starts;   // the piece is the whole unit / holds the unit's first block
     int t_first, t_last; // teams that hold the unit's pieces
-    int absent;          // (block kernel) some page of its keys is absent
 };
 
 // A warp's walk over the units of its team's piece of the line.
@@ -254,7 +261,7 @@ struct Walk {
             blocks = s.blocks;
             lo = s.lo;
             if (s.regular) {
-                blocks = static_cast<int>(prefix_blocks(s, p, k + 1) - prefix_blocks(s, p, k));
+                blocks = prefix_blocks(s, p, k + 1) - prefix_blocks(s, p, k);
                 lo = first_key(s, p, k);
             }
         } else {
@@ -267,9 +274,9 @@ struct Walk {
                 to = min(to, from + step);
             }
             k = from;
-            const int before = static_cast<int>(prefix_blocks(s, p, k));
+            const int before = prefix_blocks(s, p, k);
             u0 = head0 + before;
-            len = blocks = static_cast<int>(prefix_blocks(s, p, k + 1) - before);
+            len = blocks = prefix_blocks(s, p, k + 1) - before;
             lo = first_key(s, p, k);
         }
         int b0, b1;
