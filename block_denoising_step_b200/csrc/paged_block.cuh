@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 f *= w2;
             }
         }
+        const float masked = CAP ? -8.f / (fac * inv_cap) : 0.f;
         int jj = 0, unit_no = 0;  // jj: tile counter of the CTA
         bool ok = true;
         while (ok && next_piece()) {
@@ -634,6 +635,11 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             p[e] = H2::pack(p0, p1);
                         }
                     } else if (small) {  // capped_small in pairs, its powers of 1 / cap in the coefficients
+                        // masked scores: at u = -8 the fit, of odd degree with a positive end, is below -10^6 caps
+                        if (cut) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = fmaxf(x[e], masked);
+                        }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const f32x2 v = pair(x[2 * e], x[2 * e + 1]), z = mul2(v, v);
@@ -641,11 +647,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             q = fma2(z, q, pair(tc[1], tc[1]));
                             q = fma2(z, q, pair(tc[0], tc[0]));
                             const float2 y = unpair(fma2(mul2(v, z), q, fma2(v, fac2, nmu2)));
-                            float p0 = ex2(y.x), p1 = ex2(y.y);
-                            if (cut) {
-                                p0 = x[2 * e] == -INFINITY ? 0.f : p0;
-                                p1 = x[2 * e + 1] == -INFINITY ? 0.f : p1;
-                            }
+                            const float p0 = ex2(y.x), p1 = ex2(y.y);
                             ls[e & 1] = add2(ls[e & 1], pair(p0, p1));
                             p[e] = H2::pack(p0, p1);
                         }

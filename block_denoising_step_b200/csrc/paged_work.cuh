@@ -40,6 +40,7 @@ struct SeqInfo {
 struct Partition {
     int G, R, TS, KB, log2_kb, causal, window;
     int tokens;              // of a super tile: R / G * TS
+    int unit_cost;           // blocks that starting and ending a unit takes the time of
     int align;               // blocks start at multiples of it: KB, or 1 where sequences have one tile
     int rows_min, rows_max;  // query rows per KV head of the sequences this launch takes
 };
@@ -132,12 +133,14 @@ __device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partitio
     return s;
 }
 // Its length on the line, and the line's up to it (`before` the chunk).  cut > 0:
-// the line counts pieces of `cut` blocks of each unit, else blocks.
+// the line counts pieces of `cut` blocks of each unit, else blocks, with unit_cost
+// empty ones before each unit's (CTAs with many short units took up to 1.5 times as
+// long without).
 __device__ __forceinline__ void place(SeqInfo& s, const CacheView& c, const Partition& p, int cut, int before, int lane) {
     if (cut > 0)
         s.head = s.tiles * (s.blocks <= cut ? 1 : (s.blocks + cut - 1) / cut);
     else
-        s.head = s.regular ? prefix_blocks(s, p, s.tiles) : s.tiles * s.blocks;
+        s.head = (s.regular ? prefix_blocks(s, p, s.tiles) : s.tiles * s.blocks) + s.tiles * p.unit_cost;
     s.end = before + warp_inclusive(s.head * c.Hkv, lane);
 }
 
@@ -255,7 +258,7 @@ struct Walk {
         // the super tile: the last k with prefix(k) <= x
         int k, u0, blocks, lo, len;  // len: the unit's length on the line
         if (cut > 0 || !s.regular) {
-            len = cut <= 0 ? s.blocks : s.blocks <= cut ? 1 : (s.blocks + cut - 1) / cut;
+            len = cut <= 0 ? s.blocks + p.unit_cost : s.blocks <= cut ? 1 : (s.blocks + cut - 1) / cut;
             k = s.tiles == 1 ? 0 : x / len;
             u0 = head0 + k * len;
             blocks = s.blocks;
@@ -268,26 +271,33 @@ struct Walk {
             int from = 0, to = s.tiles;  // prefix(from) <= x < prefix(to)
             while (to - from > 1) {
                 const int step = (to - from + 31) / 32, at = from + lane * step;
-                const bool le = at < to && prefix_blocks(s, p, at) <= x;
+                const bool le = at < to && prefix_blocks(s, p, at) + at * p.unit_cost <= x;
                 const int cnt = __popc(__ballot_sync(0xffffffffu, le));
                 from += (cnt - 1) * step;
                 to = min(to, from + step);
             }
             k = from;
             const int before = prefix_blocks(s, p, k);
-            u0 = head0 + before;
-            len = blocks = prefix_blocks(s, p, k + 1) - before;
+            u0 = head0 + before + k * p.unit_cost;
+            blocks = prefix_blocks(s, p, k + 1) - before;
+            len = blocks + p.unit_cost;
             lo = first_key(s, p, k);
         }
         int b0, b1;
+        bool starts, ends;  // the piece has the unit's beginning, its end
         if (cut > 0) {
             b0 = min((t - u0) * cut, blocks);
             b1 = min(b0 + cut, blocks);
+            starts = t == u0;
+            ends = t == u0 + len - 1;
             ++t;
         } else {
-            b0 = t - u0;
-            b1 = min(t_end - u0, blocks);
-            t = u0 + b1;
+            const int e0 = t - u0, e1 = min(t_end - u0, len);
+            starts = e0 == 0;
+            ends = e1 == len;
+            b0 = max(e0 - p.unit_cost, 0);
+            b1 = max(e1 - p.unit_cost, 0);
+            t = u0 + e1;
         }
         q.end = 0;
         q.b = s.b;
@@ -298,8 +308,8 @@ struct Walk {
         q.rows = min(p.R, s.n * p.G - q.row0);
         q.t_first = per == 1 ? u0 : u0 / per;
         q.t_last = cut > 0 && len == 1 ? q.t_first : per == 1 ? u0 + len - 1 : (u0 + len - 1) / per;
-        q.whole = cut > 0 ? len == 1 : b0 == 0 && b1 == blocks;
-        q.starts = cut > 0 ? t - 1 == u0 : b0 == 0;
+        q.whole = starts && ends;
+        q.starts = starts;
         q.n = 0;
         q.hi = 0;
         q.key0 = lo;
