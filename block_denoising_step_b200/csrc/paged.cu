@@ -124,7 +124,7 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     a.p.align = rows_most <= S::R ? 1 : a.p.KB;
     a.p.TS = 1;
     a.p.tokens = S::R / a.p.G;
-    a.p.unit_cost = 1;
+    a.p.unit_cost = 3;
     auto kern = paged::paged_split_kernel<HD, ES, BF, NT>;
     set_smem_attr_once(kern, S::BYTES, dev);
     static std::atomic<int> per_sm{0};  // resident CTAs per SM: a property of the kernel
@@ -139,7 +139,7 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
     const int64_t tiles = std::min<int64_t>(rows, rows / S::R + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + a.p.KB - 1) / a.p.KB;
-    if (tiles * (blocks + 1) >= INT32_MAX) return DGEN_EINVAL;  // (rows <= 2^31, blocks <= 2^24: no overflow)
+    if (tiles * (blocks + 3) >= INT32_MAX) return DGEN_EINVAL;  // (rows <= 2^31, blocks <= 2^24: no overflow)
     grid = std::max<int64_t>(1, std::min(grid, tiles * blocks));
     if (2 * static_cast<size_t>(grid) * S::R * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
     a.counters = ws.counters;
@@ -199,7 +199,7 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     a.p.KB = a.p.align = paged::kBlkKeys;
     a.p.log2_kb = 7;
     int log2_br = 3;
-    while (log2_br < 7 && a.c.page % (2 << log2_br) == 0) ++log2_br;
+    while ((1 << log2_br) < L::VR && a.c.page % (2 << log2_br) == 0) ++log2_br;  // box rows: at most a V stage's
     CUtensorMap tq, tk, tv;
     {
         const cuuint64_t ts = a.c.n_tokens > 1 ? a.q.ts * 2 : static_cast<cuuint64_t>(a.Hq) * HD * 2;
@@ -222,10 +222,10 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     for (int ts : {4, 2})
         if (a.p.TS == 1 && (ts == 2 || !a.c.cu) && 8 * avg >= 7 * ((avg + ts - 1) / ts * ts)) a.p.TS = ts;
     a.p.tokens = tokens * a.p.TS;
-    a.p.unit_cost = 3;
+    a.p.unit_cost = 4;
     const int64_t units = std::min<int64_t>(rows, rows / (a.p.R * a.p.TS) + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + 2 * paged::kBlkKeys - 2) / paged::kBlkKeys;
-    if (units * (blocks + 3) >= INT32_MAX) return DGEN_EINVAL;
+    if (units * (blocks + 4) >= INT32_MAX) return DGEN_EINVAL;
     const int64_t teams = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid) / a.p.TS, units * blocks));
     const int64_t grid = teams * a.p.TS;
     if (2 * static_cast<size_t>(grid) * paged::kBlkRows * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
@@ -336,7 +336,7 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     a.scale = scale;
     a.cap = cap;
     a.q_bf16 = type == DGEN_TYPE_BF16;
-    a.min_blocks = 2;
+    a.min_blocks = 1;
     Workspace ws{static_cast<unsigned int*>(workspace), static_cast<int*>(workspace) + kMaxGrid,
                  reinterpret_cast<paged::Piece*>(static_cast<uint8_t*>(workspace) + kCounterBytes),
                  reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeadBytes),

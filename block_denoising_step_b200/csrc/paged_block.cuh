@@ -53,7 +53,11 @@ struct BlockLayout {
     static constexpr int NB = HD == 256 ? 2 : 3;      // score buffers in tensor memory
     static constexpr int THREADS = 384;               // four role warps, two warpgroups of softmax
     static constexpr int Q_BYTES = kBlkRows * HD * 2; // HD / 64 boxes of [128 rows x 128 B]
-    static constexpr int STAGE = kBlkKeys * SC * 2;   // SC / 64 boxes of [128 rows x 128 B]
+    static constexpr int STAGE = kBlkKeys * SC * 2;   // K: SC / 64 boxes of [128 rows x 128 B]
+    // V: at hd 256 64 keys x 256 columns, so that one product covers all of them (N = 256: 128 cycles, half the
+    // instructions for the issuing thread, and time for it to signal and wait in), else as K
+    static constexpr int VR = HD == 256 ? 64 : kBlkKeys;
+    static constexpr int VB = STAGE / (VR * 128);     // boxes of [VR rows x 128 B]
     static constexpr int STAGES = HD == 64 ? 8 : 5;
     static constexpr int KV_OFF = Q_BYTES;
     static constexpr int M_OFF = KV_OFF + STAGES * STAGE;  // float m[2][128]: the running maximum, by tile parity
@@ -315,29 +319,32 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             const int live = min(s.hi - k0, kBlkKeys);
             const uint32_t have = __ballot_sync(0xffffffffu, row != kNoRow);
             const uint32_t absent = ~have & ((1u << nbox) - 1u);
+            // rows to clear: the copies then report to a barrier of their own, and kv_full follows the clearing
+            const bool clear = is_v && (live < kBlkKeys || absent != 0);
+            const int stage_rows = is_v ? L::VR : kBlkKeys, boxes = is_v ? L::VB : L::SC / 64;
 #pragma unroll
             for (int n = 0; n < L::NS; ++n) {
                 const int st = (at + n) % ST;
                 const uint32_t ph = ((at + n) / ST) & 1;
+                // V at hd 256: stage n holds the keys 64 n .., else (and K): the columns SC n .. of all keys
+                const bool by_keys = is_v && L::VR < kBlkKeys;
+                const int r0 = by_keys ? n * L::VR : 0, x0 = by_keys ? 0 : n * L::SC;
+                const uint32_t mine = by_keys ? ((1u << (L::VR >> log2_br)) - 1u) << (r0 >> log2_br) : 0xFFFFFFFFu;
                 if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[st], ph ^ 1u, err, ERR_BLOCK_PRODUCER))) {
                     ok = false;
                     return;
                 }
-                // rows to clear: the copies then report to a barrier of their own, and kv_full follows the clearing
-                const bool clear = is_v && (live < kBlkKeys || absent != 0);
                 uint64_t* done = clear ? tail : &kv_full[st];
-                if (leader) mbar_expect_tx(done, __popc(have) * br * 128 * (L::SC / 64));
+                if (leader) mbar_expect_tx(done, __popc(have & mine) * br * 128 * boxes);
                 __syncwarp();
                 // (issued by one thread: copies of several lanes go out one by one at twice the cost)
-                for (uint32_t left = have; left != 0; left &= left - 1) {
-                    const int box = __ffs(left) - 1;
-                    const int r = static_cast<int>(__shfl_sync(0xffffffffu, row, box));
-                    const uint32_t dst = sKV + st * L::STAGE + (box << log2_br) * 128;
-                    if (leader) {
-#pragma unroll
-                        for (int x = 0; x < L::SC / 64; ++x)
-                            tma_load_2d(dst + x * (kBlkKeys * 128), tm, n * L::SC + x * 64, r, smem_u32(done));
-                    }
+                for (uint32_t left = have & mine; left != 0; left &= left - 1) {
+                    const int part = __ffs(left) - 1;
+                    const int r = static_cast<int>(__shfl_sync(0xffffffffu, row, part));
+                    const uint32_t dst = sKV + st * L::STAGE + ((part << log2_br) - r0) * 128;
+                    if (leader)
+                        for (int x = 0; x < boxes; ++x)
+                            tma_load_2d(dst + x * (stage_rows * 128), tm, x0 + x * 64, r, smem_u32(done));
                 }
                 pending |= 1u << st;
                 fill_ph = (fill_ph & ~(1u << st)) | (ph << st);
@@ -347,11 +354,11 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                         return;
                     }
                     tail_ph ^= 1u;
-                    constexpr int CH = L::SC / 8;  // 16-byte chunks of a stage row (which is cleared whole: no swizzle)
-                    for (int i = lane; i < kBlkKeys * CH; i += 32) {
+                    constexpr int CH = L::VB * 8;  // 16-byte chunks of a stage row (which is cleared whole: no swizzle)
+                    for (int i = lane; i < L::VR * CH; i += 32) {
                         const int r = i / CH, ch = i % CH;
-                        if (r >= live || ((absent >> (r >> log2_br)) & 1u))
-                            *reinterpret_cast<uint4*>(smem + L::KV_OFF + st * L::STAGE + (ch >> 3) * (kBlkKeys * 128) +
+                        if (r0 + r >= live || ((absent >> ((r0 + r) >> log2_br)) & 1u))
+                            *reinterpret_cast<uint4*>(smem + L::KV_OFF + st * L::STAGE + (ch >> 3) * (L::VR * 128) +
                                                       r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             constexpr uint32_t type = BF ? (1u << 7) | (1u << 10) : 0u;  // operand types bf16 / f16
             constexpr uint32_t base = (1u << 4) | type | (static_cast<uint32_t>(kBlkRows >> 4) << 24);
             constexpr uint32_t idesc_s = base | (static_cast<uint32_t>(kBlkKeys >> 3) << 17);
-            constexpr uint32_t idesc_pv = base | (1u << 16) | (static_cast<uint32_t>(L::SC >> 3) << 17);
+            constexpr uint32_t idesc_pv = base | (1u << 16) | (static_cast<uint32_t>(HD >> 3) << 17);  // N = hd
             int st = 0, unit_no = 0;
             int buf = 0, sbuf = 0;      // score buffers of the next P V and the next S
             uint32_t p_ph = 0;          // phase of p_full[buf]
@@ -461,10 +468,11 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t vd0 = sdesc_sw128_mn(sKV + st * L::STAGE, kBlkKeys * 128);
+                        const uint64_t vd0 = sdesc_sw128_mn(sKV + st * L::STAGE, L::VR * 128);
 #pragma unroll
-                        for (int kk = 0; kk < kBlkKeys / 16; ++kk)
-                            mma_ts(x * L::SC, tp + kk * 8, vd0 + kk * (2048 / 16), idesc_pv, kk > 0 ? 1u : more);
+                        for (int kk = 0; kk < L::VR / 16; ++kk)
+                            mma_ts(0, tp + x * (L::VR / 2) + kk * 8, vd0 + kk * (2048 / 16), idesc_pv,
+                                   x > 0 || kk > 0 ? 1u : more);
                         mma_commit(smem_u32(&kv_empty[st]));
                         if (++st == ST) {
                             st = 0;
