@@ -116,14 +116,16 @@ struct Workspace {
 template <int HD, int ES, bool BF, int NT>
 int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const Workspace& ws, int64_t rows_most) {
     using S = paged::SplitSmem<HD, ES, NT>;
-    a.p.R = S::R;
+    // whole tokens per row tile, where a token's rows fit one (the walk counts a tile's keys by its tokens)
+    const bool tokens_fit = a.p.G <= S::R;
+    a.p.R = tokens_fit ? S::R / a.p.G * a.p.G : S::R;
     a.p.KB = paged::SplitLayout<HD, ES, NT>::BLOCK_KEYS;
     a.p.log2_kb = a.p.KB == 64 ? 6 : 7;
     static_assert(paged::SplitLayout<HD, ES, NT>::BLOCK_KEYS == 64 || paged::SplitLayout<HD, ES, NT>::BLOCK_KEYS == 128,
                   "log2_kb");
-    a.p.align = rows_most <= S::R ? 1 : a.p.KB;
+    a.p.align = rows_most <= a.p.R || !tokens_fit ? 1 : a.p.KB;
     a.p.TS = 1;
-    a.p.tokens = S::R / a.p.G;
+    a.p.tokens = std::max(1, a.p.R / a.p.G);
     a.p.unit_cost = 3;
     auto kern = paged::paged_split_kernel<HD, ES, BF, NT>;
     set_smem_attr_once(kern, S::BYTES, dev);
@@ -137,7 +139,7 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     int64_t grid = std::min(kMaxGrid, sms * per_sm.load(std::memory_order_relaxed));
     // no more CTAs than blocks of the longest possible line
     const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
-    const int64_t tiles = std::min<int64_t>(rows, rows / S::R + a.c.B) * a.c.Hkv;
+    const int64_t tiles = std::min<int64_t>(rows, rows / a.p.R + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + a.p.KB - 1) / a.p.KB;
     if (tiles * (blocks + 3) >= INT32_MAX) return DGEN_EINVAL;  // (rows <= 2^31, blocks <= 2^24: no overflow)
     grid = std::max<int64_t>(1, std::min(grid, tiles * blocks));

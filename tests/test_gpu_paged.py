@@ -120,6 +120,19 @@ def test_many_new_tokens(hd, workspace):
         check_attention(cache, q, new, workspace, causal=True, window=200)
 
 
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("kind,page,group", [("bf16-e4m3", 16, 3), ("f16-e4m3", 7, 7), ("bf16", 7, 3), ("f16", 12, 5),
+                                             ("bf16", 7, 48), ("bf16", 16, 7), ("f16", 8, 3)])
+def test_many_new_tokens_of_odd_groups(hd, kind, page, group, workspace):
+    """Groups that do not divide a row tile, on either kernel (E4M3 caches and odd pages take the split one)."""
+    lens, new = [500, 41, 316, 64], [237, 41, 100, 1]
+    cache = make_cache(kind, lens, 1, hd, page, seed=60)
+    q = (2 * torch.randn(sum(new), group, hd, generator=_gen(61), device="cuda")).to(TYPES[kind][0])
+    check_attention(cache, q, new, workspace, causal=True)
+    check_attention(cache, q, new, workspace, causal=True, window=70)
+    check_attention(cache, q, new, workspace, causal=False, window=33, cap=20.0)
+
+
 @pytest.mark.parametrize("new", [1, 128])
 def test_absent_pages_are_masked(new, workspace):
     lens = [400, 300, 128]
