@@ -17,6 +17,10 @@
 // and page), then all threads sweep (row, 8 + 8 elements) items.  A thread's next
 // items are on their way while it writes the current ones, the first ones already
 // while the pages are looked up, which their addresses do not need.
+//
+// Measured on a B200 (device time of a replayed graph): prompts of up to 4,096 tokens in 16
+// sequences, 32 query heads on 8 of 128 into E4M3 pages, 153 us (5.3 TB/s); eight canvases of
+// 256 tokens, 16 heads on 8 of 256, 16 us (4.2 TB/s); one token 3.0 us (launch latency).
 #pragma once
 
 #include "paged.cuh"

@@ -31,6 +31,12 @@
 // split kernel would add half as many products again.  Its error is that of one
 // rounding per weight, averaged over the keys, below the output's own rounding.
 //
+// Measured on a B200 (device time of a replayed graph): eight canvases of 256 tokens over
+// 4,352 keys, 16 heads on 8 of 256, 128 us (1,137 TFLOP/s; tensor cores); one over 2,304 keys
+// 24 us (five blocks per CTA: start-up and join outweigh them); six ragged causal chunks of up
+// to 1,024 tokens over 5,000 keys, 32 heads on 8 of 128, capped scores, 277 to 303 us (the
+// capped scores' fp32 work).
+//
 // Keys behind the sequence's end and absent pages are not loaded; scores there
 // are replaced by -inf, and the V rows are zeros (shared memory may hold anything).  Every wait is bounded; on a timeout the kernel records an
 // error, drains its own copies and MMAs, frees its tensor memory and exits.
@@ -776,7 +782,8 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
 // of CTA c's row tile of the unit that starts in its team and goes on behind it, if
 // there is one (a.joins, written by the scheduler).  A launch of its own, because a
 // row tile's pieces are up to 128 KB each: the CTA that finishes last would read
-// them alone (80 us for one canvas of 256 tokens at hd 256).
+// them alone (one canvas of 256 tokens over 2,304 keys at hd 256: 132 us so, 45 with this
+// launch and scores read twice instead of kept; 24 now).
 constexpr int kJoinCols = 16;
 template <int HD, bool BF>
 __global__ void __launch_bounds__(256) paged_block_join_kernel(const AttendArgs a) {

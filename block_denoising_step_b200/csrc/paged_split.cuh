@@ -24,6 +24,12 @@
 // scaled by a power of two per row into fp16's range; the head's scales enter
 // the score factor and the output.  A pair of ldmatrix b16 lanes holds four
 // bytes, so the k order within 16 elements is permuted alike in K and Q.
+//
+// Measured on a B200 (device time of a replayed graph): 131,071 keys of 8 heads x 128 for
+// one token 89 us (6.05 TB/s); 64 tokens over up to 8,192 keys of 8 x 256 323 us (6.9 TB/s);
+// 48 tokens over up to 16,384 E4M3 keys of 8 x 128 189 us (4.4 TB/s: the conversions bound it);
+// 128 tokens in windows of 1,024 keys of 12 x 64 74 us (4.8 TB/s: the start and end of short
+// units); one token over 301 keys 8.8 us (the chain of dependent loads and the join).
 #pragma once
 
 #include "mma_sync.cuh"
@@ -70,6 +76,7 @@ struct SplitSmem {
     static constexpr int PIECE_OFF = FLAG_OFF + 16;                     // the current piece and the next
     static constexpr int WALK_OFF = PIECE_OFF + 2 * 64;                 // Walk[32]: warp 0's, a lane each
     static constexpr int BYTES = (WALK_OFF + 32 * static_cast<int>(sizeof(Walk)) + 15) & ~15;
+    static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
 // chunk position of chunk c in row r: eight rows of one chunk column fall into

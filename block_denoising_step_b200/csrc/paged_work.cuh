@@ -135,7 +135,8 @@ __device__ __forceinline__ SeqInfo load_chunk(const CacheView& c, const Partitio
 // Its length on the line, and the line's up to it (`before` the chunk).  cut > 0:
 // the line counts pieces of `cut` blocks of each unit, else blocks, with unit_cost
 // empty ones before each unit's (CTAs with many short units took up to 1.5 times as
-// long without).
+// long without: a ragged batch of prompt chunks 397 us instead of 286, 1,536 windows
+// of 1,024 keys 90 us instead of 74).
 __device__ __forceinline__ void place(SeqInfo& s, const CacheView& c, const Partition& p, int cut, int before, int lane) {
     if (cut > 0)
         s.head = s.tiles * (s.blocks <= cut ? 1 : (s.blocks + cut - 1) / cut);
@@ -207,14 +208,14 @@ struct Walk {
         total = before;
         per = (total + teams - 1) / teams;
         cut = 0;
-        if (2 * units <= teams) {
+        if (units > 0 && 2 * units <= teams) {
             // fewer units than teams: each cut by itself, one piece a team.  Even lengths take all teams' share,
             // others pieces of T / (teams - units), of which there are at most T / that + units = teams.
             cut = nominal == units * most ? (most + teams / units - 1) / (teams / units)
                                           : (nominal + teams - units - 1) / (teams - units);
             if (cut < min_blocks) cut = min_blocks;
             if (most <= cut + kWholeSlack) cut = most;
-        } else if (static_cast<long long>((units + teams - 1) / teams) * most <= per + kWholeSlack) {
+        } else if (units > 0 && static_cast<long long>((units + teams - 1) / teams) * most <= per + kWholeSlack) {
             cut = most;  // whole units
         }
         if (cut > 0) {
