@@ -153,10 +153,10 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
 }
 
 // Row tiles of 8, 16 or (hd <= 128: the accumulators of 32 rows of 256 would not
-// fit the registers) 32 query rows, by the rows a sequence has on average.
+// fit the registers) 32 query rows, by the rows a sequence of this launch has on average.
 template <int HD, int ES, bool BF>
 int split_rows(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, const Workspace& ws, int64_t most) {
-    const int64_t rows = (static_cast<int64_t>(a.c.n_tokens) + a.c.B - 1) / a.c.B * a.p.G;
+    const int64_t rows = std::min<int64_t>((static_cast<int64_t>(a.c.n_tokens) + a.c.B - 1) / a.c.B * a.p.G, a.p.rows_max);
     if (rows <= 8) return launch_split<HD, ES, BF, 1>(st, dev, sms, a, ws, most);
     if constexpr (HD <= 128)
         if (rows > 16) return launch_split<HD, ES, BF, 4>(st, dev, sms, a, ws, most);
@@ -171,8 +171,12 @@ int split_hd(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, cons
     return split_rows<HD, 2, false>(st, dev, sms, a, ws, most);
 }
 
-// Rows per KV head of one sequence above which the tcgen05 kernel takes it.
-constexpr int kBlockMinRows = 32;
+// Rows per KV head of one sequence above which the tcgen05 kernel takes it, although its tiles hold 128: it
+// reads the keys once for all of them.  Split kernel / tcgen05 kernel in us, 8 KV heads, lengths of 4,352 keys in
+// 16 sequences (and one of 301): hd 128, 8 rows 51 / 50 (9.8 / 11.1), 16 rows 57 / 51 (13.9 / 11.1), 24 rows
+// 100 / 52; hd 256, 8 rows 99 / 91 (12.9 / 15.5), 16 rows 111 / 94 (19.7 / 15.5), 24 rows 195 / 94; hd 64, whose
+// short rows the split kernel streams with more warps, 16 rows 37 / 43 (10.7 / 14.0), 24 rows 53 / 42 (14.0 / 14.1).
+constexpr int block_min_rows(int hd) { return hd >= 128 ? 8 : 16; }
 
 // Whether the tcgen05 kernel can take this call's long sequences: 16-bit cache, a
 // group that fits a row tile, pages that TMA boxes of 8 rows or more divide, and
@@ -216,8 +220,9 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
             !encode_16bit(&tv, a.c.v, 2, kdims, kstrides, kbox))
             return DGEN_EINVAL;
     }
-    // teams of 4 or 2 row tiles where the average sequence's tiles fill them to 7/8; of 2 at most for a ragged
-    // batch, whose last teams have idle members
+    // teams of 4 or 2 row tiles where the average sequence's tiles fill them to 7/8 (eight canvases of 256 tokens
+    // over 4,352 keys: 132 us in fours, 145 in twos or alone; even chunks of 1,024 tokens 699, 719, 731); of 2 at most
+    // for a ragged batch, whose last teams have idle members (ragged chunks 289 us in twos, 307 in fours, 293 alone)
     const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
     const int64_t avg = std::max<int64_t>(1, (rows / a.c.B + a.p.R - 1) / a.p.R);
     a.p.TS = 1;
@@ -245,7 +250,7 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
                : DGEN_ECUDA;
 }
 
-// Sequences with more than kBlockMinRows query rows per KV head go to the tcgen05
+// Sequences with more than block_min_rows query rows per KV head go to the tcgen05
 // kernel, the others to the split kernel; a ragged batch may hold both kinds, and
 // each launch passes over the other's.
 template <int HD>
@@ -253,14 +258,16 @@ int attend_hd(cudaStream_t st, int dev, int sms, const dgen_paged_cache* c, page
     // the most rows one sequence has if none is without a new token (where some are, the split kernel also
     // takes longer ones): a decode batch given with cu_new costs no second launch
     const int64_t most = (a.c.cu ? std::max(a.c.n_tokens - a.c.B + 1, 1) : a.c.n_uniform) * static_cast<int64_t>(a.p.G);
-    const bool block = block_fits(c, a) && most > kBlockMinRows;
+    constexpr int min_rows = block_min_rows(HD);
+    const bool block = block_fits(c, a) && most > min_rows;
     if (block) {
         paged::AttendArgs b = a;
-        b.p.rows_min = kBlockMinRows + 1;
+        b.p.rows_min = min_rows + 1;
         const int rc = c->type == DGEN_TYPE_BF16 ? launch_block<HD, true>(st, dev, sms, b, ws)
                                                  : launch_block<HD, false>(st, dev, sms, b, ws);
-        if (rc != DGEN_OK || !a.c.cu) return rc;
-        a.p.rows_max = kBlockMinRows;
+        // (a single token's rows alone can pass the limit: then no sequence is left)
+        if (rc != DGEN_OK || !a.c.cu || a.p.G > min_rows) return rc;
+        a.p.rows_max = min_rows;
     }
     return split_hd<HD>(st, dev, sms, a, ws, c->type, std::min<int64_t>(most, a.p.rows_max));
 }

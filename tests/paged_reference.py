@@ -97,10 +97,10 @@ def attention(cache, q, new, *, scale=None, causal=True, window=0, cap=0.0):
             if j.numel():
                 worst = torch.where(see, ds, 0.0).amax(1)
                 # weights off by e^ds, the sum likewise; P in 16-bit halves (2^-16), or rounded once: to the row
-                # type for more than 32 rows per KV head on a 16-bit cache, to fp16 for bf16 rows on an E4M3
-                # cache; fp32 sums over the keys; fp16 weights at worst 2^-25 absolute per key
+                # type for more than 8 rows per KV head (16 at hd 64) on a 16-bit cache, to fp16 for bf16 rows
+                # on an E4M3 cache; fp32 sums over the keys; fp16 weights at worst 2^-25 absolute per key
                 p_step = 2.0 ** -16
-                if cache.k_scale is None and n * g > 32:
+                if cache.k_scale is None and n * g > (8 if hd >= 128 else 16):
                     p_step = torch.finfo(q.dtype).eps / 2
                 elif cache.k_scale is not None and q.dtype == torch.bfloat16:
                     p_step = 2.0 ** -11

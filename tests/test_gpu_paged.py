@@ -121,6 +121,18 @@ def test_many_new_tokens(hd, workspace):
 
 
 @pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 4, 8, 9, 16, 17])
+def test_rows_around_the_kernels_limit(hd, group, workspace):
+    """A batch whose sequences have 8, 9, 16 and 17 rows per KV head, or about: few go to one kernel, more to the other."""
+    for new in ([1, 1, 1, 1, 0], [8, 9, 16, 17, 1], [2, 2, 2, 2, 2]):
+        lens = [300, 19, 641, 128, 77]
+        cache = make_cache("bf16", lens, 2, hd, 16, seed=70)
+        q = (2 * torch.randn(sum(new), 2 * group, hd, generator=_gen(71), device="cuda")).to(torch.bfloat16)
+        check_attention(cache, q, new, workspace, causal=True)
+        check_attention(cache, q, new, workspace, causal=False, window=50, cap=20.0)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("kind,page,group", [("bf16-e4m3", 16, 3), ("f16-e4m3", 7, 7), ("bf16", 7, 3), ("f16", 12, 5),
                                              ("bf16", 7, 48), ("bf16", 16, 7), ("f16", 8, 3)])
 def test_many_new_tokens_of_odd_groups(hd, kind, page, group, workspace):
