@@ -186,6 +186,8 @@ def paged_attention(cache: PagedCache, q, out, workspace, cu_new=None, scale: fl
         cu = cu_new.data_ptr()
     elif n % cache.batch:
         _bad("dgen_paged_attention", "without cu_new every sequence has the same number of rows")
+    if not 0 <= window < 1 << 31:
+        _bad("dgen_paged_attention", "window: wants 0 (none) or a count of positions below 2^31")
     args = (cache._ref, n, cu, _ROW_TYPES[dtype], heads, _pack(q.data_ptr(), st[0], st[1]),
             _pack(out.data_ptr(), so[0], so[1]), cache._scale if scale is None else scale, 1 if causal else 0, window,
             cap, lse_at, workspace.data_ptr(), workspace.numel(),

@@ -105,6 +105,17 @@ def test_binding_refuses_what_is_not_a_cuda_cache():
         assert e.value.status == dg.DGEN_EINVAL
 
 
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5, -1])
+def test_binding_refuses_windows_beyond_32_bits(window):
+    """They would reach the C call as another window (2^32 + 5 as 5)."""
+    cache = object.__new__(dg.paged.PagedCache)
+    cache._dev, cache._row_types, cache.head_dim, cache.batch = -1, (torch.bfloat16,), 64, 1
+    q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(dg.DgenError) as e:
+        dg.paged_attention(cache, q, q.clone(), torch.zeros(64, dtype=torch.uint8), window=window)
+    assert e.value.status == dg.DGEN_EINVAL
+
+
 class _Cpu:
     def __init__(self, k, v, table, lens):
         self.k, self.v, self.page_table, self.kv_len, self.k_scale, self.v_scale = k, v, table, lens, None, None
