@@ -29,7 +29,8 @@
 // memory delivers; with N = 128 it is 8 KB per 64.
 // P is rounded once to the operand type (bf16 / fp16): hi + lo parts as in the
 // split kernel would add half as many products again.  Its error is that of one
-// rounding per weight, averaged over the keys, below the output's own rounding.
+// rounding per weight: averaged over the keys where many count, as large as the
+// output's own rounding where few do.
 //
 // Measured on a B200 (device time of a replayed graph): eight canvases of 256 tokens over
 // 4,352 keys, 16 heads on 8 of 256, 128 us (1,137 TFLOP/s; tensor cores); one over 2,304 keys
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     using L = BlockLayout<HD>;
     using H2 = Half2<BF>;
     constexpr int NB = L::NB, ST = L::STAGES;
+    constexpr float LIFT = BF ? 0.f : kHalfLift;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem), sQ = sbase, sKV = sbase + L::KV_OFF;
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     l_run *= m_run == -INFINITY ? 0.f : ex2(m_run - m_new);
                     m_run = m_new;
                 }
-                const float mu = m_run == -INFINITY ? 0.f : m_run;
+                const float mu = m_run == -INFINITY ? 0.f : m_run - LIFT;
                 if (__any_sync(0xffffffffu, move && j > 0)) {  // rescale O rows, after the P V before this one
                     const float corr = move ? (m_prev == -INFINITY ? 0.f : ex2(m_prev - m_new)) : 1.f;
                     if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(t - 1) % NB], ((t - 1) / NB) & 1, err,
@@ -726,6 +728,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[last % NB], (last / NB) & 1, err, ERR_BLOCK_SOFTMAX)))
                     break;
                 tc_fence_after();
+                m -= LIFT;
                 jj += n;
                 ++unit_no;
             }

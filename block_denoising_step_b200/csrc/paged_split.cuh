@@ -10,8 +10,9 @@
 // of a group of up to 8 heads wastes nothing that matters: S^T = K Q^T
 // (16 keys x 8 rows per instruction), O^T += V^T P^T.  P^T's operand layout is
 // S^T's accumulator layout transposed 8 x 8 (movmatrix).  P is kept as hi + lo
-// 16-bit parts (about 16 significant bits), so the output's own rounding is the
-// only one that shows; with an E4M3 cache and bf16 rows fp16's 11 bits alone do.
+// 16-bit parts (about 16 significant bits, fp16's down to 2^-16 of the largest weight), so the
+// output's own rounding is the only one that shows; with an E4M3 cache and bf16 rows fp16's 11
+// bits alone do (2^-12 of a weight against the output's 2^-9).
 //
 // Memory-bound: every visible K and V row is read once.  Each warp streams its
 // own tiles of 16 or 32 keys through a private ring of shared memory (cp.async 16 bytes,
@@ -123,6 +124,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
     using S = SplitSmem<HD, ES, NT>;
     using H2 = Half2<BF>;
     constexpr int R = S::R, CH = L::CH, ST = L::STAGES, QCH = HD / 8, MT = L::MT, KEYS = L::KEYS;
+    constexpr float LIFT = BF ? 0.f : kHalfLift;
     constexpr uint32_t kAllKeys = KEYS == 32 ? 0xFFFFFFFFu : (1u << KEYS) - 1u;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
                         float p[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+                            const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1] - LIFT;
                             p[e] = ex2(sc[km][nt][e] - mu);
                             l_run[nt][e & 1] += p[e];
                         }
@@ -584,10 +586,10 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
                 l += s_l[w * R + r] * (s_m[w * R + r] == -INFINITY ? 1.f : exp2f(s_m[w * R + r] - m));
             }
             if (s.whole) {
-                store4(a, s, out_bf, vscale, r, col, v, m, l);
+                store4(a, s, out_bf, vscale, r, col, v, m - LIFT, l);
             } else {
                 __stcg(reinterpret_cast<float4*>(part_o(a, HD, slot, r) + col), v);
-                if (col == 0) __stcg(reinterpret_cast<float2*>(part_ml(a, HD, slot, r)), make_float2(m, l));
+                if (col == 0) __stcg(reinterpret_cast<float2*>(part_ml(a, HD, slot, r)), make_float2(m - LIFT, l));
             }
         }
         if (!s.whole) {

@@ -531,7 +531,8 @@ int dgen_paged_append(const dgen_paged_cache* cache, int32_t n_tokens, const int
  * are fp32; the weights P enter the second product in about 16 bits (up to 8
  * query rows of a sequence per KV head, up to 16 at head_dim 64, and any count over
  * pages of a size that 8 does not divide or an E4M3 cache with fp16 rows), in fp16
- * (bf16 rows over an E4M3 cache) or rounded once to the row type; the output is
+ * (bf16 rows over an E4M3 cache) or rounded once to the row type; fp16 weights and
+ * halves lose at most 2^-32 of the row's largest weight below that; the output is
  * rounded once.  Cached values
  * inside a sequence are taken to be finite; nothing behind its end is used.
  * workspace: 16-byte aligned device memory of dgen_paged_workspace_bytes(),

@@ -1,0 +1,78 @@
+"""The paged cache's operators at the edges of what their calls allow, against bounds that count each rounding."""
+import math
+
+import pytest
+import torch
+
+import block_denoising_step_b200 as dg
+from tests import paged_bounds as bounds
+from tests import paged_reference as ref
+from tests.test_gpu_paged import TYPES, _gen, cu_of, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def workspace():
+    return dg.paged_workspace()
+
+
+def check(cache, q, new, workspace, uniform=False, **kw):
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    dg.paged_attention(cache, q, out, workspace, cu_new=None if uniform else cu_of(new), lse=lse, **kw)
+    dg.paged_synchronize(workspace)
+    steps = [bounds.p_step(cache, q, n * q.shape[1] // cache.n_kv_heads) for n in new if n]
+    step, half = max(s for s, _ in steps), steps[0][1]
+    want, want_lse, bound, lse_bound = bounds.attention(cache, q, new, p_step=step, p_half=half, **kw)
+    n = sum(new)
+    bad = (out.double() - want).abs()[:n] > (ref.half_step(q.dtype, want) * (1 + 2.0 ** -7) + bound)[:n]
+    assert not bad.any() and not out[:n].isnan().any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+    live = want_lse[:n] > -math.inf
+    assert torch.equal(lse[:n] == -math.inf, ~live)
+    assert not ((lse[:n].double() - want_lse[:n]).abs()[live] > lse_bound[:n][live]).any()
+    assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()
+    return out, lse
+
+
+# ------------------------------------------------------------------ weights in 16 bits
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 64])
+@pytest.mark.parametrize("below", [64.5, 6.5, 0.48])
+def test_light_keys_beside_heavy_ones(kind, hd, new, below, workspace):
+    """Every 16th key outweighs the others by 2^24 / below and has no value: the output is the light keys' alone."""
+    t, ct = TYPES[kind]
+    length = 640 + new
+    cache = make_cache(kind, [length], 1, hd, 16, seed=120)
+    g = _gen(121)
+    heavy = torch.arange(16, device="cuda") % 16 == 5
+    cache.k.copy_(torch.zeros(cache.k.shape, device="cuda"))
+    cache.k[..., ~heavy, 0] = torch.full((1,), -1.0, device="cuda").to(ct)
+    value = 64 * (1 + torch.rand(cache.v.shape, generator=g, device="cuda"))
+    value[..., heavy, :] = 0
+    cache.v.copy_(value)
+    if cache.k_scale is not None:
+        cache.k_scale.fill_(1.0), cache.v_scale.fill_(512.0)
+    else:
+        cache.v.mul_(16)
+    q = torch.zeros(new, 2, hd, device="cuda", dtype=t)
+    q[..., 0] = 1
+    check(cache, q, [new], workspace, causal=False, scale=math.log(2) * math.log2(2 ** 24 / below))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_weights_of_few_rows_keep_16_bits(kind, hd, workspace):
+    """Two keys whose values nearly cancel: what a weight's rounding loses is left over."""
+    cache = make_cache(kind, [2], 1, hd, 8, seed=130)
+    ct, page = TYPES[kind][1], int(cache.page_table[0, 0])
+    cache.k[page, 0, :2], cache.v[page, 0, :2] = torch.zeros(2, hd, device="cuda").to(ct), 0.0
+    if cache.k_scale is not None:
+        cache.k_scale.fill_(1.0), cache.v_scale.fill_(1.0)
+    cache.k[page, 0, 1, 0] = -1.0
+    cache.v[page, 0, 0], cache.v[page, 0, 1] = 0.75, -1.0
+    q = torch.zeros(1, 8, hd, device="cuda", dtype=TYPES[kind][0])
+    q[0, :, 0] = 0.2 + 0.03 * torch.arange(8, device="cuda").to(q.dtype)
+    check(cache, q, [1], workspace, scale=1.0)
