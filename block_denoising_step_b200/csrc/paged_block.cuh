@@ -170,9 +170,10 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int base) {
     return up & ~dn;
 }
 
-// Masks 32 scores of the tile's columns c0 .. (keys k0 ..): outside [lo, hi), or in
-// an absent page part.
-__device__ __forceinline__ void mask_scores(float (&x)[32], int lo, int hi, int k0, int c0, uint32_t have, int log2_br) {
+// Sets 32 scores of the tile's columns c0 .. (keys k0 ..) to `none` outside [lo, hi) and
+// in absent page parts.
+__device__ __forceinline__ void mask_scores(float (&x)[32], int lo, int hi, int k0, int c0, uint32_t have, int log2_br,
+                                            float none) {
     uint32_t parts = 0;
     if (log2_br >= 5) {
         parts = (have >> (c0 >> log2_br)) & 1u ? 0xFFFFFFFFu : 0u;
@@ -183,7 +184,7 @@ __device__ __forceinline__ void mask_scores(float (&x)[32], int lo, int hi, int 
     const uint32_t bits = range_bits(lo, hi, k0) & parts;
 #pragma unroll
     for (int e = 0; e < 32; ++e)
-        if (!((bits >> e) & 1u)) x[e] = -INFINITY;
+        if (!((bits >> e) & 1u)) x[e] = none;
 }
 
 // Partial results of this kernel: [slot][hd / 4][128 rows] float4, so that a warp
@@ -569,13 +570,14 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
                 auto look = [&](float(&x)[32], int c0) {
+                    // (with a cap NaN, which maximum and minimum both pass over: what is masked chooses nothing)
+                    if (cut) mask_scores(x, vlo, vhi, k0 + c0, c0, have, log2_br, CAP ? NAN : -INFINITY);
                     if constexpr (CAP) {
-                        float lo[4] = {mn, x[1], x[2], x[3]};
+                        float lo[4] = {mn, INFINITY, INFINITY, INFINITY};
 #pragma unroll
                         for (int e = 0; e < 16; ++e) lo[e & 3] = min3(lo[e & 3], x[2 * e], x[2 * e + 1]);
                         mn = fminf(fminf(lo[0], lo[1]), fminf(lo[2], lo[3]));
                     }
-                    if (cut) mask_scores(x, vlo, vhi, k0 + c0, c0, have, log2_br);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) mx[e & 3] = max3(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 };
@@ -593,8 +595,10 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 bool small = false;
                 float mt = raw * fac;
                 if constexpr (CAP) {
-                    small = __all_sync(0xffffffffu, (raw == -INFINITY || fabsf(mt * inv_cap) <= kTanhSmall) &&
-                                                        fabsf(mn * fac * inv_cap) <= kTanhSmall);
+                    // (rows behind the tile's last hold whatever was there: they have no say in which form is taken)
+                    small = __all_sync(0xffffffffu, row >= rows || raw == -INFINITY ||
+                                                        (fabsf(mt * inv_cap) <= kTanhSmall &&
+                                                         fabsf(mn * fac * inv_cap) <= kTanhSmall));
                     if (raw > -INFINITY)
                         mt = small ? capped_small(mt, mt * inv_cap) : capped_any(mt * inv_cap, kLog2e * a.cap);
                 }
@@ -683,18 +687,19 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     }
                     tmem_st16(tb + 64 + c0 / 2, p);
                 };
-                // columns 96 .., 64 .., 32 .., 0 ..
+                // columns 96 .. (left from above), 64 .., 32 .., 0 ..
+                if (CAP && cut) mask_scores(xb, vlo, vhi, k0 + 96, 96, have, log2_br, -INFINITY);
 #pragma unroll 1
                 for (int c0 = 64; c0 >= 0; c0 -= 64) {
                     weigh(xb, c0 + 32);
                     scores_wait(xa);
                     if (c0 > 0) scores_start(tb + 32, xb);
-                    if (cut) mask_scores(xa, vlo, vhi, k0 + c0, c0, have, log2_br);
+                    if (cut) mask_scores(xa, vlo, vhi, k0 + c0, c0, have, log2_br, -INFINITY);
                     weigh(xa, c0);
                     if (c0 > 0) {
                         scores_wait(xb);
                         scores_start(tb, xa);
-                        if (cut) mask_scores(xb, vlo, vhi, k0 + 32, 32, have, log2_br);
+                        if (cut) mask_scores(xb, vlo, vhi, k0 + 32, 32, have, log2_br, -INFINITY);
                     }
                 }
                 const float2 lsum = unpair(add2(ls[0], ls[1]));

@@ -35,6 +35,38 @@ def check(cache, q, new, workspace, uniform=False, **kw):
     return out, lse
 
 
+# ------------------------------------------------------------------ capped scores
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("group,new", [(3, [45, 20]), (7, [60, 1]), (4, [100, 33])])
+def test_capped_results_depend_on_the_sequences_alone(kind, group, new, workspace):
+    """Keys behind the end, padding rows, the other sequence and earlier calls change no bit."""
+    t = TYPES[kind][0]
+    cache = make_cache(kind, [333, 90], 1, 128, 16, seed=110)
+    cache.k.nan_to_num_(0.0), cache.v.nan_to_num_(0.0)
+    ids, n = cache.page_table.cpu(), sum(new)
+    q = torch.full((n + 40, group, 128), 0.0, device="cuda", dtype=t)
+    q[:n] = (2 * torch.randn(n, group, 128, generator=_gen(111), device="cuda")).to(t)
+    other = make_cache(kind, [1000], 1, 128, 16, seed=112, std=50.0)
+    noise = (50 * torch.randn(200, group, 128, generator=_gen(113), device="cuda")).to(t)
+    first = None
+    for tail, pad, disturb in ((0.0, 0.0, False), (200.0, 100.0, True), (-200.0, math.nan, True), (math.nan, -3.0, False)):
+        for b, length in ((0, 333), (1, 90)):
+            cache.k[ids[b, length // 16], :, length % 16:] = tail
+            cache.v[ids[b, length // 16], :, length % 16:] = tail
+        q[n:] = pad
+        if disturb:
+            dg.paged_attention(other, noise, torch.empty_like(noise), workspace, cap=9.0)
+        got = check(cache, q, new, workspace, cap=30.0, causal=True)
+        if first is None:
+            first = got
+        assert torch.equal(got[0][:n], first[0][:n]) and torch.equal(got[1][:n], first[1][:n])
+    q[new[0]:n] *= 100  # the other sequence's scores pass the cap
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    dg.paged_attention(cache, q, out, workspace, cu_new=cu_of(new), lse=lse, cap=30.0)
+    assert torch.equal(out[:new[0]], first[0][:new[0]]) and torch.equal(lse[:new[0]], first[1][:new[0]])
+
+
 # ------------------------------------------------------------------ weights in 16 bits
 
 @pytest.mark.parametrize("kind", list(TYPES))
