@@ -236,7 +236,10 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     const int64_t teams = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid) / a.p.TS, units * blocks));
     const int64_t grid = teams * a.p.TS;
     if (2 * static_cast<size_t>(grid) * paged::kBlkRows * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
-    auto kern = a.cap > 0.f ? paged::paged_block_kernel<HD, BF, true> : paged::paged_block_kernel<HD, BF, false>;
+    const paged::Cap cap = paged::cap_form(a.scale, a.cap);
+    auto kern = cap == paged::Cap::none    ? paged::paged_block_kernel<HD, BF, paged::Cap::none>
+                : cap == paged::Cap::usual ? paged::paged_block_kernel<HD, BF, paged::Cap::usual>
+                                           : paged::paged_block_kernel<HD, BF, paged::Cap::any>;
     a.joins = ws.joins;
     set_smem_attr_once(kern, L::SMEM_BYTES, dev);
     a.parts = ws.parts;
@@ -343,7 +346,9 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     a.lse = lse;
     a.Hq = n_q_heads;
     a.scale = scale;
-    a.cap = cap;
+    // Within 2^-100 .. 2^126 the kernels' factors stay in fp32's range; a cap beyond acts as the nearer limit does:
+    // scores below 2^-100 weigh alike, and those that 2^126 bends are so far apart that one key takes all.
+    a.cap = cap > 0.f ? std::clamp(cap, 0x1p-100f, 0x1p126f) : 0.f;
     a.q_bf16 = type == DGEN_TYPE_BF16;
     a.min_blocks = 1;
     Workspace ws{static_cast<unsigned int*>(workspace), static_cast<int*>(workspace) + kMaxGrid,

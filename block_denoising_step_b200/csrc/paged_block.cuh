@@ -50,6 +50,16 @@ namespace paged {
 
 enum : int { ERR_BLOCK_PRODUCER = 20, ERR_BLOCK_MMA = 21, ERR_BLOCK_SOFTMAX = 22, ERR_BLOCK_DRAIN = 23, ERR_BLOCK_PIECE = 24 };
 
+// Caps on the scores: none; usual ones, whose tanh is a polynomial of a tile's raw scores with the powers of scale /
+// cap in its coefficients; any other, whose powers leave fp32's range: the form is chosen and computed per score.
+enum class Cap { none, usual, any };
+inline Cap cap_form(float scale, float cap) {
+    if (cap <= 0.f) return Cap::none;
+    const double fac = static_cast<double>(scale) * kLog2e, w2 = fac * kLn2 / cap * (fac * kLn2 / cap);
+    const double last = fac * w2 * w2 * w2 * w2;  // of the last coefficient, which is 0.0153 of it
+    return last >= 0x1p-119 && last <= 0x1p100 ? Cap::usual : Cap::any;
+}
+
 constexpr int kBlkKeys = 128;
 constexpr int kBlkRows = 128;
 
@@ -209,7 +219,7 @@ struct Parts {
     }
 };
 
-template <int HD, bool BF, bool CAP>
+template <int HD, bool BF, Cap CAP>
 __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     paged_block_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const AttendArgs a, int log2_br, int* __restrict__ err) {
@@ -523,7 +533,6 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 f *= w2;
             }
         }
-        const float masked = CAP ? -8.f / (fac * inv_cap) : 0.f;
         int jj = 0, unit_no = 0;  // jj: tile counter of the CTA
         bool ok = true;
         while (ok && next_piece()) {
@@ -571,8 +580,8 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
                 auto look = [&](float(&x)[32], int c0) {
                     // (with a cap NaN, which maximum and minimum both pass over: what is masked chooses nothing)
-                    if (cut) mask_scores(x, vlo, vhi, k0 + c0, c0, have, log2_br, CAP ? NAN : -INFINITY);
-                    if constexpr (CAP) {
+                    if (cut) mask_scores(x, vlo, vhi, k0 + c0, c0, have, log2_br, CAP != Cap::none ? NAN : -INFINITY);
+                    if constexpr (CAP == Cap::usual) {
                         float lo[4] = {mn, INFINITY, INFINITY, INFINITY};
 #pragma unroll
                         for (int e = 0; e < 16; ++e) lo[e & 3] = min3(lo[e & 3], x[2 * e], x[2 * e + 1]);
@@ -594,13 +603,16 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 bool small = false;
                 float mt = raw * fac;
-                if constexpr (CAP) {
+                if constexpr (CAP != Cap::none) {
+                    const float u = mt * inv_cap;
                     // (rows behind the tile's last hold whatever was there: they have no say in which form is taken)
-                    small = __all_sync(0xffffffffu, row >= rows || raw == -INFINITY ||
-                                                        (fabsf(mt * inv_cap) <= kTanhSmall &&
-                                                         fabsf(mn * fac * inv_cap) <= kTanhSmall));
+                    if constexpr (CAP == Cap::usual)
+                        small = __all_sync(0xffffffffu, row >= rows || raw == -INFINITY ||
+                                                            (fabsf(u) <= kTanhSmall &&
+                                                             fabsf(mn * fac * inv_cap) <= kTanhSmall));
                     if (raw > -INFINITY)
-                        mt = small ? capped_small(mt, mt * inv_cap) : capped_any(mt * inv_cap, kLog2e * a.cap);
+                        mt = (CAP == Cap::usual ? small : fabsf(u) <= kTanhSmall) ? capped_small(mt, u)
+                                                                                 : capped_any(u, kLog2e * a.cap);
                 }
                 // the maximum after the tile before this one, from the other warpgroup
                 float m_prev = -INFINITY;
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                 // P of 32 columns c0 .. over columns 64 + c0 / 2 .. of S_j, whose scores have been read by then
                 auto weigh = [&](float(&x)[32], int c0) {
                     uint32_t p[16];
-                    if constexpr (!CAP) {
+                    if constexpr (CAP == Cap::none) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float2 y = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), fac2, nmu2));
@@ -655,11 +667,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             p[e] = H2::pack(p0, p1);
                         }
                     } else if (small) {  // capped_small in pairs, its powers of 1 / cap in the coefficients
-                        // masked scores: at u = -8 the fit, of odd degree with a positive end, is below -10^6 caps
-                        if (cut) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = fmaxf(x[e], masked);
-                        }
+                        // (a masked -inf stays -inf: v z is, and q, whose leading coefficient is positive, is +inf)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const f32x2 v = pair(x[2 * e], x[2 * e + 1]), z = mul2(v, v);
@@ -678,8 +686,9 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                             float pe[2];
 #pragma unroll
                             for (int w = 0; w < 2; ++w) {
-                                const float v = x[2 * e + w];
-                                pe[w] = v == -INFINITY ? 0.f : ex2(capped_any(v * fac * inv_cap, cap2) - mu);
+                                const float y = x[2 * e + w] * fac, u = y * inv_cap;
+                                const float f = CAP == Cap::any && fabsf(u) <= kTanhSmall ? capped_small(y, u) : capped_any(u, cap2);
+                                pe[w] = y == -INFINITY ? 0.f : ex2(f - mu);
                             }
                             ls[e & 1] = add2(ls[e & 1], pair(pe[0], pe[1]));
                             p[e] = H2::pack(pe[0], pe[1]);
@@ -688,7 +697,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     tmem_st16(tb + 64 + c0 / 2, p);
                 };
                 // columns 96 .. (left from above), 64 .., 32 .., 0 ..
-                if (CAP && cut) mask_scores(xb, vlo, vhi, k0 + 96, 96, have, log2_br, -INFINITY);
+                if (CAP != Cap::none && cut) mask_scores(xb, vlo, vhi, k0 + 96, 96, have, log2_br, -INFINITY);
 #pragma unroll 1
                 for (int c0 = 64; c0 >= 0; c0 -= 64) {
                     weigh(xb, c0 + 32);

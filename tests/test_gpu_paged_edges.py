@@ -37,6 +37,25 @@ def check(cache, q, new, workspace, uniform=False, **kw):
 
 # ------------------------------------------------------------------ capped scores
 
+# (cap, scale, deviation of the queries): scores far below the cap, all about zero, saturated; powers of scale / cap
+# beyond fp32's range
+CAPS = [(1e5, None, 2.0), (18000.0, None, 2.0), (1e30, None, 2.0), (3e38, None, 2.0), (1e-6, None, 0.0),
+        (1e-6, None, 1e-7), (1e-30, None, 2.0), (1e-42, None, 2.0), (1e-42, None, 0.0), (50.0, 1e-4, 2.0), (50.0, 3e-4, 2.0),
+        (1.0, 1e-30, 2.0), (4.0, None, 2.0)]
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("cap,scale,dev", CAPS)
+@pytest.mark.parametrize("new", [[70, 40], [1, 1]], ids=["many", "few"])
+def test_caps_of_any_size(hd, cap, scale, dev, new, workspace):
+    for kind in ("bf16", "f16"):
+        cache = make_cache(kind, [300, 200], 2, hd, 16, seed=100)
+        cache.page_table[1, 3] = -1
+        q = (dev * torch.randn(sum(new), 6, hd, generator=_gen(101), device="cuda")).to(TYPES[kind][0])
+        check(cache, q, new, workspace, cap=cap, scale=scale)
+        check(cache, q, new, workspace, cap=cap, scale=scale, causal=False, window=90)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("group,new", [(3, [45, 20]), (7, [60, 1]), (4, [100, 33])])
 def test_capped_results_depend_on_the_sequences_alone(kind, group, new, workspace):
