@@ -22,7 +22,7 @@
 // and masked: nothing behind a sequence's end is read.
 //
 // E4M3 caches: bytes are widened to fp16 (exact) in registers; queries are
-// scaled by a power of two per row into fp16's range; the head's scales enter
+// scaled by a power of two per row to the top of fp16's range; the head's scales enter
 // the score factor and the output.  A pair of ldmatrix b16 lanes holds four
 // bytes, so the k order within 16 elements is permuted alike in K and Q.
 //
@@ -218,9 +218,11 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
                 }
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                // the largest element goes to [2^14, 2^15), so that elements down to 2^-28 of it are normal numbers
+                // (the products' sum stays in fp32: 2^15 * 448 * 256 < 2^33)
                 int ex = 0;
                 if (m > 0.f && m < INFINITY) frexpf(m, &ex);
-                ex = min(max(ex, -100), 100);
+                ex = max(ex, -112) - 15;  // (2^-ex is a number of fp32)
                 const float down = ldexpf(1.f, -ex);
 #pragma unroll
                 for (int e = 0; e < PER / 2; ++e) w[e] = Half2<false>::pack(x[e].x * down, x[e].y * down);
@@ -282,7 +284,8 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float f = a.scale * kscale * (ES == 1 ? qscale[nt * 8 + 2 * t4 + j] : 1.f);
+                // (the scale first with the query's own, whose product is of the order of one)
+                const float f = a.scale * (ES == 1 ? qscale[nt * 8 + 2 * t4 + j] : 1.f) * kscale;
                 fac[nt][j] = f * kLog2e;
             }
         const float inv_cap = a.cap > 0.f ? kLn2 / a.cap : 0.f;  // of a log2-domain score

@@ -6,6 +6,9 @@ Scores are taken in powers of e.  What separates a kernel's score from the exact
   a cap c, while |s| <= 0.6 c       the fit of tanh is 1.54e-7 |u| off at most (u + u^3 P(u^2) - tanh u over u, by
                                     evaluation in 64 bits at 2 million points), and five roundings: (1.6e-7 + 5 * 2^-24) |s|
   a cap c, any other score          c tanh = c (1 - 2 / (1 + e^2u)), values of up to c in four roundings: 6 * 2^-24 c
+  queries over an E4M3 cache        as fp16 with the row's largest element at 2^14 or more: half a subnormal step is 2^-25,
+                                    so each element is off by 2^-39 of the largest at most (bf16's 8 and fp16's 11 bits
+                                    are exact above that), the score by that times scale * sum |k|
 A weight e^s is off by twice the largest of these (its own and the maximum's), by 2^-22 for the exponential, and by
 p_step for its own rounding; sums of n weights in fp32 by n * 2^-24.  fp16 weights are kept 2^7 above their
 maximum, so that what a subnormal loses is at most 2^-25 * 2^-7 of the largest weight for each key."""
@@ -50,6 +53,8 @@ def attention(cache, q, new, *, scale=None, causal=True, window=0, cap=0.0, p_st
                 qh = q[rows, head].double()
                 s = qh @ kh.T * scale
                 off = qh.abs() @ kh.abs().T * (scale * hd * 2.0 ** -24)
+                if cache.k_scale is not None:
+                    off += qh.abs().amax(1)[:, None] * kh.abs().sum(1) * (scale * 2.0 ** -39)
                 if cap:
                     s = cap * torch.tanh(s / cap)
                     small = bool((s.abs() <= 0.5 * cap)[see].all())

@@ -127,3 +127,27 @@ def test_weights_of_few_rows_keep_16_bits(kind, hd, workspace):
     q = torch.zeros(1, 8, hd, device="cuda", dtype=TYPES[kind][0])
     q[0, :, 0] = 0.2 + 0.03 * torch.arange(8, device="cuda").to(q.dtype)
     check(cache, q, [1], workspace, scale=1.0)
+
+
+@pytest.mark.parametrize("kind", ["bf16-e4m3", "f16-e4m3"])
+@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("large", [2.0 ** 13, 2.0 ** 17, 2.0 ** 20])
+def test_queries_with_one_large_element_over_e4m3(kind, new, large, workspace):
+    """Where the large element's key coordinates are zero, the small ones make the score."""
+    if kind == "f16-e4m3":
+        large = min(large, 32768.0)
+    cache = make_cache(kind, [200], 1, 128, 16, seed=140)
+    cache.k.view(torch.uint8)[..., 0] = 0
+    cache.k_scale.fill_(0.5)
+    q = torch.zeros(new, 2, 128, device="cuda")
+    q[..., 1:5] = 2.0 ** -10 * torch.randn(new, 2, 4, generator=_gen(141), device="cuda")
+    q[..., 0] = large
+    check(cache, q.to(TYPES[kind][0]), [new], workspace, scale=16.0)
+
+
+@pytest.mark.parametrize("power", [-120, -60, 60, 118, 126])
+def test_queries_of_any_magnitude_over_e4m3(power, workspace):
+    """bf16 reaches as far as fp32: the row's scale follows it."""
+    cache = make_cache("bf16-e4m3", [200], 1, 128, 16, seed=150)
+    q = (torch.randn(1, 2, 128, generator=_gen(151), device="cuda").clamp(-1.9, 1.9) * 2.0 ** power).bfloat16()
+    check(cache, q, [1], workspace, scale=2.0 ** -power / 8)
