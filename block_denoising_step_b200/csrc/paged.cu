@@ -248,7 +248,8 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
         cudaSuccess)
         return DGEN_ECUDA;
     if (teams == 1) return DGEN_OK;
-    return launch_ex(st, paged::paged_block_join_kernel<HD, BF>, dim3(a.n_ctas, HD / paged::kJoinCols), dim3(256), 0, a) == cudaSuccess
+    return launch_ex(st, paged::paged_block_join_kernel<HD, BF>, dim3(a.n_ctas, HD / paged::kJoinCols), dim3(256), 0, a,
+                     static_cast<const int*>(ws.err)) == cudaSuccess
                ? DGEN_OK
                : DGEN_ECUDA;
 }
@@ -403,8 +404,8 @@ int dgen_paged_synchronize(void* workspace, void* stream) {
         cudaStreamSynchronize(st) != cudaSuccess)
         return DGEN_ECUDA;
     if (err == 0) return DGEN_OK;
-    // the call that gave up may have left its counters in between
-    if (cudaMemsetAsync(workspace, 0, kCounterBytes, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+    // the call that gave up may have left its counters in between and its join list unfinished
+    if (cudaMemsetAsync(workspace, 0, kHeadBytes, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
         return DGEN_ECUDA;
     return DGEN_EDEVICE;
 }

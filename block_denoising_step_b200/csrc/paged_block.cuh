@@ -297,16 +297,14 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
     if (warp == 2) {
         Walk walk;
         walk.start(c, a.p, lane, a.min_blocks, blockIdx.x, a.n_ctas);
-        bool cut = false;
+        // What the join kernel has to know of the unit that starts here and goes on behind: none until it is met, so
+        // that a walk that a wait ends early leaves no record of an earlier call.
+        if (lane == 0) a.joins[blockIdx.x].end = 1;
         for (int i = 0;; ++i) {
             Piece q{};
             const bool have = walk.next(c, a.p, lane, q);
             q.end = !have;
-            // what the join kernel has to know of the unit that starts here and goes on behind
-            if (lane == 0 && (!have || (q.starts && !q.whole && q.rows > 0))) {
-                if (have || !cut) a.joins[blockIdx.x] = q;
-                cut = true;
-            }
+            if (lane == 0 && have && q.starts && !q.whole && q.rows > 0) a.joins[blockIdx.x] = q;
             if (!__all_sync(0xffffffffu,
                             mbar_wait(&piece_empty[i & 1], ((i >> 1) & 1) ^ 1, err, ERR_BLOCK_PIECE)))
                 break;
@@ -800,16 +798,17 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
 // there is one (a.joins, written by the scheduler).  A launch of its own, because a
 // row tile's pieces are up to 128 KB each: the CTA that finishes last would read
 // them alone (one canvas of 256 tokens over 2,304 keys at hd 256: 132 us so, 45 with this
-// launch and scores read twice instead of kept; 24 now).
+// launch and scores read twice instead of kept; 24 now).  Nothing is joined while the
+// workspace holds an error: pieces may be missing.
 constexpr int kJoinCols = 16;
 template <int HD, bool BF>
-__global__ void __launch_bounds__(256) paged_block_join_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(256) paged_block_join_kernel(const AttendArgs a, const int* __restrict__ err) {
     using H2 = Half2<BF>;
     pdl_enter();
     const int cta = blockIdx.x, member = cta & (a.p.TS - 1);
     const Piece s = a.joins[cta];
     const int row = threadIdx.x & (kBlkRows - 1), col = blockIdx.y * kJoinCols + (threadIdx.x >> 7) * 8;
-    if (s.end || row >= s.rows) return;
+    if (s.end || row >= s.rows || __ldcg(err) != 0) return;
     float m = -INFINITY, l = 0.f, v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.f;

@@ -549,8 +549,8 @@ int64_t dgen_paged_workspace_bytes(void);
 
 /* Waits for the stream; DGEN_EDEVICE if a device-side bounded wait ran out in a
  * dgen_paged_attention call with this workspace since the last check (its outputs
- * are then not valid; the workspace is put back to its first state), DGEN_ECUDA
- * on a CUDA error, else DGEN_OK. */
+ * and those of later calls up to the check are then not valid; the workspace is put
+ * back to its first state), DGEN_ECUDA on a CUDA error, else DGEN_OK. */
 int dgen_paged_synchronize(void* workspace, void* stream);
 
 /* Diagnostic entry point (exercised by the tests): the same product with E4M3

@@ -151,3 +151,30 @@ def test_queries_of_any_magnitude_over_e4m3(power, workspace):
     cache = make_cache("bf16-e4m3", [200], 1, 128, 16, seed=150)
     q = (torch.randn(1, 2, 128, generator=_gen(151), device="cuda").clamp(-1.9, 1.9) * 2.0 ** power).bfloat16()
     check(cache, q, [1], workspace, scale=2.0 ** -power / 8)
+
+
+# ------------------------------------------------------------------ workspaces
+
+ERROR_WORD, JOIN_LIST, HEAD = 1023, 4096, 4096 + 1023 * 64
+
+
+def test_nothing_is_joined_after_a_wait_ran_out():
+    """With an error in the workspace the pieces of cut row tiles are left alone: whoever wrote the list of them, the
+    rows it names are not written.  The check empties the list too."""
+    ws = dg.paged_workspace()
+    cache = make_cache("bf16", [2304], 2, 128, 16, seed=160)
+    q = torch.randn(256, 4, 128, generator=_gen(161), device="cuda").bfloat16()
+    good, out = torch.empty_like(q), torch.full_like(q, 7.0)
+    dg.paged_attention(cache, q, good, ws, causal=False)
+    dg.paged_synchronize(ws)
+    assert ws[JOIN_LIST:HEAD].any()
+    ws[:JOIN_LIST].view(torch.int32)[ERROR_WORD] = 22
+    dg.paged_attention(cache, q, out, ws, causal=False)
+    with pytest.raises(dg.DgenError) as e:
+        dg.paged_synchronize(ws)
+    assert e.value.status == dg.DGEN_EDEVICE
+    assert (out == 7.0).all()  # two units over all CTAs: every row tile is cut
+    assert not ws[:HEAD].any()
+    dg.paged_attention(cache, q, out, ws, causal=False)
+    dg.paged_synchronize(ws)
+    assert torch.equal(out, good)
