@@ -329,6 +329,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
         uint32_t pending = 0, fill_ph = 0, tail_ph = 0;
         const bool leader = elect_one();
         bool ok = true;
+        bool tail_open = false;  // copies that report to `tail` are on their way
         int q_phase = -1;  // parity of the last Q copy issued
         // This warp's tile of 128 keys from key k0 on into the ring from its stage number `at` on; `row` is
         // this lane's page part.  V rows that must not count (behind hi, absent pages) are cleared here.
@@ -363,13 +364,14 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                         for (int x = 0; x < boxes; ++x)
                             tma_load_2d(dst + x * (stage_rows * 128), tm, x0 + x * 64, r, smem_u32(done));
                 }
-                pending |= 1u << st;
-                fill_ph = (fill_ph & ~(1u << st)) | (ph << st);
                 if (clear) {
+                    pending &= ~(1u << st);  // (what was there before has been consumed)
+                    tail_open = true;
                     if (!__all_sync(0xffffffffu, mbar_wait(tail, tail_ph, err, ERR_BLOCK_PRODUCER))) {
                         ok = false;
                         return;
                     }
+                    tail_open = false;
                     tail_ph ^= 1u;
                     constexpr int CH = L::VB * 8;  // 16-byte chunks of a stage row (which is cleared whole: no swizzle)
                     for (int i = lane; i < L::VR * CH; i += 32) {
@@ -381,6 +383,9 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (leader) mbar_arrive(&kv_full[st]);
+                } else {
+                    pending |= 1u << st;
+                    fill_ph = (fill_ph & ~(1u << st)) | (ph << st);
                 }
             }
         };
@@ -421,6 +426,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
             // was consumed before: its wait only runs out).  Without a failure the MMA issuer has waited for
             // every copy; if it alone gave up, it did so two seconds after the last of them.
             if (q_phase >= 0) mbar_wait(q_full, q_phase, err, ERR_BLOCK_DRAIN);
+            if (tail_open) mbar_wait(tail, tail_ph, err, ERR_BLOCK_DRAIN);
             for (int i = 0; i < ST; ++i)
                 if ((pending >> i) & 1u) mbar_wait(&kv_full[i], (fill_ph >> i) & 1u, err, ERR_BLOCK_DRAIN);
         }
