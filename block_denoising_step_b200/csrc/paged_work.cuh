@@ -251,6 +251,7 @@ struct Walk {
         if (t >= t_end) return false;
         int chunk_end = __shfl_sync(0xffffffffu, mine.end, 31);
         while (t >= chunk_end) {
+            if (base + 32 >= c.B) return false;  // (never with the lengths of start(); ends the walk if they changed since)
             base += 32;
             mine = load_chunk(c, p, base, lane);
             place(mine, c, p, cut, chunk_end, lane);

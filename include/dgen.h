@@ -461,7 +461,8 @@ int dgen_sample_from_logits_noalloc(const float* logits_dev, int32_t* tok_dev, u
  * kv_len[b] its length INCLUDING the new tokens of the call, so sequence b's
  * n_b new tokens sit at positions kv_len[b] - n_b .. kv_len[b] - 1.  Table and
  * lengths are device memory read when the call runs: a captured call follows
- * their later contents.  Any page_size; entries of pages behind a sequence's
+ * their later contents (if they change while it runs, its results and the
+ * workspace's counters are not valid).  Any page_size; entries of pages behind a sequence's
  * end are never read.  An entry outside [0, n_pages) is an absent page: rows
  * for it are not written, keys in it are not attended to (an evicted range).
  * Pages may be shared by sequences that only read them.
