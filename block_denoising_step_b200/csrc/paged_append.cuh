@@ -19,7 +19,7 @@
 // while the pages are looked up, which their addresses do not need.
 //
 // Measured on a B200 (device time of a replayed graph): prompts of up to 4,096 tokens in 16
-// sequences, 32 query heads on 8 of 128 into E4M3 pages, 153 us (5.3 TB/s); eight canvases of
+// sequences, 32 query heads on 8 of 128 into E4M3 pages, 160 us (5.1 TB/s); eight canvases of
 // 256 tokens, 16 heads on 8 of 256, 16 us (4.2 TB/s); one token 3.0 us (launch latency).
 #pragma once
 
@@ -57,11 +57,12 @@ __device__ __forceinline__ int find_sequence(const CacheView& c, int tok, int la
     return b < c.B ? b : -1;
 }
 
-// x / s for E4M3: x times 1 / s, corrected by the remainder (as a division is, without
-// its special cases; an infinite quotient stays).  inv = 1 / s, s and 1 / s normal.
-__device__ __forceinline__ float scaled_down(float x, float s, float inv) {
-    const float q = x * inv, r = fmaf(fmaf(-q, s, x), inv, q);
-    return r == r ? r : q;
+// Whether q = x * (1 / s) may round to another E4M3 value than x / s does.  Both are within 2 steps of fp32 of the
+// exact quotient, so they can differ only within as many of a midpoint of E4M3 (for normal numbers: 20 zero bits
+// behind a one behind the 3 kept ones); the coarser midpoints of its subnormals are not looked at one by one.
+__device__ __forceinline__ bool near_midpoint(float q) {
+    const uint32_t u = __float_as_uint(q);
+    return (u & 0xFFFFFu) - 0x7FFF8u <= 16u || fabsf(q) < 0x1p-6f;
 }
 
 template <int HD, bool BF, bool E4M3>
@@ -183,23 +184,26 @@ __global__ void __launch_bounds__(kAppendThreads, E4M3 ? 3 : 4) paged_append_ker
                 auto pack4 = [&](float2 p, float2 r) -> uint32_t {
                     return pack2_e4m3(p.x, p.y) | (static_cast<uint32_t>(pack2_e4m3(r.x, r.y)) << 16);
                 };
-                if (s > 1e-30f && s < 1e30f) {
+                // the division where it matters: 1 / s of an extreme scale, quotients near a midpoint
+                bool divide = !(s > 0x1p-100f && s < 0x1p100f);
+                float2 qx[4], qy[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    qx[e] = make_float2(x[e].x * inv, x[e].y * inv);
+                    qy[e] = make_float2(y[e].x * inv, y[e].y * inv);
+                    divide |= near_midpoint(qx[e].x) || near_midpoint(qx[e].y) || near_midpoint(qy[e].x) || near_midpoint(qy[e].y);
+                }
+                if (divide) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[e] = make_float2(scaled_down(x[e].x, s, inv), scaled_down(x[e].y, s, inv));
-                        y[e] = make_float2(scaled_down(y[e].x, s, inv), scaled_down(y[e].y, s, inv));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] = make_float2(x[e].x / s, x[e].y / s);
-                        y[e] = make_float2(y[e].x / s, y[e].y / s);
+                        qx[e] = make_float2(x[e].x / s, x[e].y / s);
+                        qy[e] = make_float2(y[e].x / s, y[e].y / s);
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    o[e] = pack4(x[2 * e], x[2 * e + 1]);
-                    o[2 + e] = pack4(y[2 * e], y[2 * e + 1]);
+                    o[e] = pack4(qx[2 * e], qx[2 * e + 1]);
+                    o[2 + e] = pack4(qy[2 * e], qy[2 * e + 1]);
                 }
                 uint8_t* base = (is_v ? a.c.v : a.c.k) +
                                 static_cast<size_t>(row_in_page(a.c, s_page[tt], h, s_off[tt])) * HD + c * 8;

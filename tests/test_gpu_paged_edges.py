@@ -178,3 +178,32 @@ def test_nothing_is_joined_after_a_wait_ran_out():
     dg.paged_attention(cache, q, out, ws, causal=False)
     dg.paged_synchronize(ws)
     assert torch.equal(out, good)
+
+
+# ------------------------------------------------------------------ the append's division
+
+# powers of two and thirds of them (ties with many rows), both sides of 2^-100 and 2^100, the ends of fp32's range
+SCALES = [1.0, 2.0 ** -7, 3.0, 1 / 3, 0.75, 0.0123, 0.0178, 17.3, 1.0000001, 0.99999994, 5e-3, 448.0, -0.5, 2.0 ** -99,
+          2.0 ** -101, 1.7e-30, 3e-31, 2.0 ** 99, 1.3 * 2.0 ** 100, 1e-40, 1e38, 3e38, 0.0, math.inf]
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+def test_e4m3_values_are_the_divisions_to_the_bit(t):
+    """Every bf16 / fp16 value over every scale: the stored byte is that of x / scale in fp32, rounded and saturated."""
+    hkv, hd = len(SCALES), 256
+    x = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(t).view(-1, 1, hd).expand(-1, hkv, -1)
+    n = x.shape[0]
+    scale = torch.tensor(SCALES)
+    k = torch.zeros(n, hkv, 1, hd, dtype=torch.float8_e4m3fn, device="cuda")
+    v = torch.zeros_like(k)
+    cache = dg.PagedCache(k, v, torch.arange(n, dtype=torch.int32, device="cuda")[None],
+                          torch.tensor([n], dtype=torch.int32, device="cuda"), scale.cuda(), scale.flip(0).cuda())
+    rows = x.contiguous().cuda()
+    dg.paged_append(cache, rows, rows)
+    for got, s in ((k, scale), (v, scale.flip(0))):
+        q = x.float() / s[None, :, None]
+        want = q.clamp(-448, 448).to(torch.float8_e4m3fn)  # (clamp keeps NaN)
+        same = got.cpu()[:, :, 0].view(torch.uint8) == want.view(torch.uint8)
+        nan = want.float().isnan()
+        assert torch.equal(got.cpu()[:, :, 0].float().isnan(), nan)
+        assert (same | nan).all(), [(SCALES[h], int((~same & ~nan)[:, h].sum())) for h in range(hkv)]
