@@ -7,6 +7,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
+#include <utility>
 
 #include "dgen.h"
 #include "launch.cuh"
@@ -42,6 +44,16 @@ bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr
 bool good_rows(const dgen_token_rows* r, int tokens, int heads) {
     return r && aligned16(r->dev) && (tokens == 1 || r->token_stride % 8 == 0) &&
            (heads == 1 || r->head_stride % 8 == 0);
+}
+
+// Rows that are written: as above, and no two of them share an element (the longer of the two strides passes over all
+// rows of the shorter one, and that over a row)
+bool good_rows_out(const dgen_token_rows* r, int tokens, int heads, int hd) {
+    if (!good_rows(r, tokens, heads)) return false;
+    int64_t ts = tokens > 1 ? std::abs(r->token_stride) : INT64_MAX, hs = heads > 1 ? std::abs(r->head_stride) : INT64_MAX;
+    int inner = ts < hs ? tokens : heads;
+    if (ts < hs) std::swap(ts, hs);  // hs: the shorter
+    return hs >= hd && (ts == INT64_MAX || (ts - hd) / hs >= inner - 1);
 }
 
 paged::RowsView view(const dgen_token_rows* r) {
@@ -287,7 +299,8 @@ int append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (n_tokens == 0) return DGEN_OK;
     if (!good_rows(k, n_tokens, cache->n_kv_heads) || !good_rows(v, n_tokens, cache->n_kv_heads)) return DGEN_EINVAL;
     if ((n_q_heads > 0) != (q != nullptr) || !q != !q_out) return DGEN_EINVAL;
-    if (q && (!good_rows(q, n_tokens, n_q_heads) || !good_rows(q_out, n_tokens, n_q_heads))) return DGEN_EINVAL;
+    if (q && (!good_rows(q, n_tokens, n_q_heads) || !good_rows_out(q_out, n_tokens, n_q_heads, cache->head_dim)))
+        return DGEN_EINVAL;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DGEN_ECUDA;
     const int sms = sm_count(dev);
@@ -328,7 +341,7 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (!std::isfinite(scale) || !(scale > 0.f) || !(cap >= 0.f) || std::isinf(cap) || window < 0 || (causal != 0 && causal != 1))
         return DGEN_EINVAL;
     if (n_tokens == 0) return DGEN_OK;
-    if (!good_rows(q, n_tokens, n_q_heads) || !good_rows(out, n_tokens, n_q_heads)) return DGEN_EINVAL;
+    if (!good_rows(q, n_tokens, n_q_heads) || !good_rows_out(out, n_tokens, n_q_heads, cache->head_dim)) return DGEN_EINVAL;
     if (!aligned16(workspace)) return DGEN_EINVAL;
     if (workspace_bytes < static_cast<int64_t>(kHeadBytes)) return DGEN_ESCRATCH;
     int dev = 0;

@@ -469,7 +469,8 @@ int dgen_sample_from_logits_noalloc(const float* logits_dev, int32_t* tok_dev, u
  *
  * Token rows are packed: [tokens][heads][head_dim] views whose last dimension is
  * contiguous and whose strides (in elements) are multiples of 8, the base
- * 16-byte aligned (e.g. parts of one fused QKV output).  cu_new [batch + 1]
+ * 16-byte aligned (e.g. parts of one fused QKV output).  Rows that are written
+ * do not overlap.  cu_new [batch + 1]
  * holds each sequence's first row (ascending, cu_new[0] = 0); NULL = n_tokens /
  * batch rows each.  Sequences may have no new token.  Rows at and behind
  * cu_new[batch] are padding: neither read nor written.  A new token whose

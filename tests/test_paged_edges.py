@@ -1,0 +1,33 @@
+"""The paged cache's calls at the edges of what they allow, what needs no GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import block_denoising_step_b200 as dg
+from tests.test_paged import A, _append, _attend, _cache, _rows
+
+
+# ------------------------------------------------------------------ output rows that overlap
+
+# (token stride, head stride) of two rows of four heads of 64
+OVERLAPPING = [(256, 0), (0, 64), (192, 64), (256, 56), (64, 64), (0, 0), (72, 128), (-192, 64)]
+APART = [(256, 64), (264, 64), (512, 128), (64, 128), (-256, 64), (256, -64)]
+
+
+@pytest.mark.parametrize("ts,hs", OVERLAPPING)
+def test_output_rows_that_overlap_are_refused(ts, hs):
+    r = _rows(ts=ts, hs=hs)
+    assert _attend(out=r) == dg.DGEN_EINVAL
+    assert _append(q_out=r) == dg.DGEN_EINVAL
+
+
+@pytest.mark.parametrize("ts,hs", APART)
+def test_output_rows_that_do_not_overlap_pass(ts, hs):
+    """(The small workspace is what the call is refused for.)"""
+    assert _attend(out=_rows(ts=ts, hs=hs), ws_bytes=16) == dg.DGEN_ESCRATCH
+
+
+def test_inputs_may_overlap():
+    """One row for all tokens or heads is read as often as it is named."""
+    assert _attend(q=_rows(ts=0, hs=0), ws_bytes=16) == dg.DGEN_ESCRATCH
