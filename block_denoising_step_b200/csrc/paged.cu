@@ -25,6 +25,7 @@ constexpr size_t kCounterBytes = (kMaxGrid + 1) * sizeof(unsigned int);  // and 
 constexpr size_t kHeadBytes = kCounterBytes + kMaxGrid * 64;             // and the block kernel's join list
 static_assert(sizeof(paged::Piece) <= 64, "join list");
 constexpr int kMaxDevices = 64;
+constexpr int kMaxHeads = 65536;         // query or KV heads: a token's rows and items count in 32 bits
 constexpr int kMaxSplitCtas = 4;         // CTAs per SM of the split kernel at most
 
 int sm_count(int dev) {
@@ -66,7 +67,7 @@ int check_cache(const dgen_paged_cache* c, int n_tokens, const int32_t* cu) {
     if ((c->type == DGEN_TYPE_E4M3) != (c->k_scale_dev != nullptr) || !c->k_scale_dev != !c->v_scale_dev)
         return DGEN_EINVAL;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DGEN_EINVAL;
-    if (c->n_pages < 1 || c->n_kv_heads < 1 || c->page_size < 1 || c->batch < 1 || c->table_pages < 1 ||
+    if (c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > kMaxHeads || c->page_size < 1 || c->batch < 1 || c->table_pages < 1 ||
         c->table_stride < c->table_pages)
         return DGEN_EINVAL;
     const int64_t rows = static_cast<int64_t>(c->n_pages) * c->n_kv_heads;  // rows of the cache count in 32 bits
@@ -104,7 +105,7 @@ paged::CacheView view(const dgen_paged_cache* c, int n_tokens, const int32_t* cu
 
 template <int HD, bool BF, bool E4M3>
 int launch_append(cudaStream_t st, const paged::AppendArgs& a, int per_block) {
-    const int blocks = (a.c.n_tokens + per_block - 1) / per_block;
+    const int blocks = a.c.n_tokens / per_block + (a.c.n_tokens % per_block != 0);
     return launch_ex(st, paged::paged_append_kernel<HD, BF, E4M3>, dim3(blocks), dim3(paged::kAppendThreads), 0, a,
                      per_block) == cudaSuccess
                ? DGEN_OK
@@ -295,7 +296,7 @@ int append(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (rc != DGEN_OK) return rc;
     if (type != DGEN_TYPE_BF16 && type != DGEN_TYPE_F16) return DGEN_EINVAL;
     if (cache->type != DGEN_TYPE_E4M3 && cache->type != type) return DGEN_EINVAL;
-    if (n_q_heads < 0 || n_q_heads > 65536 || !(rope_base >= 0.f) || std::isinf(rope_base)) return DGEN_EINVAL;
+    if (n_q_heads < 0 || n_q_heads > kMaxHeads || !(rope_base >= 0.f) || std::isinf(rope_base)) return DGEN_EINVAL;
     if (n_tokens == 0) return DGEN_OK;
     if (!good_rows(k, n_tokens, cache->n_kv_heads) || !good_rows(v, n_tokens, cache->n_kv_heads)) return DGEN_EINVAL;
     if ((n_q_heads > 0) != (q != nullptr) || !q != !q_out) return DGEN_EINVAL;

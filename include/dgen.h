@@ -498,7 +498,7 @@ typedef struct dgen_paged_cache {
     const int32_t* kv_len_dev;     /* [batch] */
     int32_t type;
     int32_t n_pages;               /* n_pages * n_kv_heads * page_size < 2^32 - 1 */
-    int32_t n_kv_heads;
+    int32_t n_kv_heads;            /* <= 65536, as n_q_heads of the append */
     int32_t page_size;
     int32_t head_dim;
     int32_t batch;

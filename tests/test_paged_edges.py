@@ -31,3 +31,13 @@ def test_output_rows_that_do_not_overlap_pass(ts, hs):
 def test_inputs_may_overlap():
     """One row for all tokens or heads is read as often as it is named."""
     assert _attend(q=_rows(ts=0, hs=0), ws_bytes=16) == dg.DGEN_ESCRATCH
+
+
+# ------------------------------------------------------------------ counts at their ends
+
+@pytest.mark.parametrize("heads", [65537, 1 << 29, 1 << 30])
+def test_more_kv_heads_than_query_heads_may_be_are_refused(heads):
+    """The append counts a token's items in 32 bits: 2^30 heads of 64 would come to none, and be divided by."""
+    c, r = _cache(n_pages=1, n_kv_heads=heads, page_size=1), _rows()
+    assert dg._lib.dgen_paged_append(ctypes.byref(c), 2, None, 0, r, r, 0, None, None, 0.0, None) == dg.DGEN_EINVAL
+    assert _attend(c, heads=heads) == dg.DGEN_EINVAL
