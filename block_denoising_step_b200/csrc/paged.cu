@@ -40,6 +40,7 @@ int sm_count(int dev) {
 }
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }  // (or null)
 
 // 16-byte access to every row: base and strides (of dimensions above one)
 bool good_rows(const dgen_token_rows* r, int tokens, int heads) {
@@ -65,6 +66,9 @@ int check_cache(const dgen_paged_cache* c, int n_tokens, const int32_t* cu) {
     if (!c || !aligned16(c->k_dev) || !aligned16(c->v_dev) || !c->page_table_dev || !c->kv_len_dev) return DGEN_EINVAL;
     if (c->type != DGEN_TYPE_BF16 && c->type != DGEN_TYPE_F16 && c->type != DGEN_TYPE_E4M3) return DGEN_EINVAL;
     if ((c->type == DGEN_TYPE_E4M3) != (c->k_scale_dev != nullptr) || !c->k_scale_dev != !c->v_scale_dev)
+        return DGEN_EINVAL;
+    if (!aligned4(c->page_table_dev) || !aligned4(c->kv_len_dev) || !aligned4(c->k_scale_dev) ||
+        !aligned4(c->v_scale_dev) || !aligned4(cu))
         return DGEN_EINVAL;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DGEN_EINVAL;
     if (c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > kMaxHeads || c->page_size < 1 || c->batch < 1 || c->table_pages < 1 ||
@@ -343,7 +347,7 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
         return DGEN_EINVAL;
     if (n_tokens == 0) return DGEN_OK;
     if (!good_rows(q, n_tokens, n_q_heads) || !good_rows_out(out, n_tokens, n_q_heads, cache->head_dim)) return DGEN_EINVAL;
-    if (!aligned16(workspace)) return DGEN_EINVAL;
+    if (!aligned16(workspace) || !aligned4(lse)) return DGEN_EINVAL;
     if (workspace_bytes < static_cast<int64_t>(kHeadBytes)) return DGEN_ESCRATCH;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DGEN_ECUDA;

@@ -41,3 +41,22 @@ def test_more_kv_heads_than_query_heads_may_be_are_refused(heads):
     c, r = _cache(n_pages=1, n_kv_heads=heads, page_size=1), _rows()
     assert dg._lib.dgen_paged_append(ctypes.byref(c), 2, None, 0, r, r, 0, None, None, 0.0, None) == dg.DGEN_EINVAL
     assert _attend(c, heads=heads) == dg.DGEN_EINVAL
+
+
+# ------------------------------------------------------------------ alignment of what is read by 32-bit words
+
+@pytest.mark.parametrize("field", ["page_table_dev", "kv_len_dev", "k_scale_dev", "v_scale_dev"])
+def test_misaligned_words_of_the_cache_are_refused(field):
+    c = dict(type=2, k_scale_dev=A, v_scale_dev=A) if "scale" in field else {}
+    c[field] = A + 2
+    assert _append(_cache(**c)) == dg.DGEN_EINVAL
+    assert _attend(_cache(**c), ws_bytes=16) == dg.DGEN_EINVAL
+
+
+def test_misaligned_counts_and_lse_are_refused():
+    assert _append(cu=A + 1) == dg.DGEN_EINVAL
+    assert _attend(cu=A + 1, ws_bytes=16) == dg.DGEN_EINVAL
+    r = _rows()
+    for at, status in ((A + 2, dg.DGEN_EINVAL), (A + 4, dg.DGEN_ESCRATCH)):
+        assert dg._lib.dgen_paged_attention(ctypes.byref(_cache()), 2, None, 0, 4, r, r, 0.125, 1, 0, 0.0, at, A, 16,
+                                            None) == status
