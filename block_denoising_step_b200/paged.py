@@ -40,6 +40,7 @@ class PagedCache:
         _need(k.is_contiguous() and v.is_contiguous(), call, "k and v must be contiguous")
         _need(page_table.dim() == 2 and page_table.dtype == torch.int32 and
               (page_table.stride(1) == 1 or page_table.shape[1] == 1), call, "page_table: [batch][pages] int32")
+        _need(page_table.shape[0] > 0, call, "page_table: no sequence")
         _need(kv_len.shape == page_table.shape[:1] and kv_len.dtype == torch.int32 and kv_len.is_contiguous(), call,
               "kv_len: [batch] int32")
         e4m3 = k.dtype == torch.float8_e4m3fn
@@ -147,7 +148,7 @@ def paged_append(cache: PagedCache, k, v, q=None, q_out=None, cu_new=None, rope_
     if cu_new is not None:
         _check_cu("dgen_paged_append", cache, cu_new)
         cu = cu_new.data_ptr()
-    elif n % cache.batch:
+    elif cache.batch < 1 or n % cache.batch:
         _bad("dgen_paged_append", "without cu_new every sequence has the same number of rows")
     args = (cache._ref, n, cu, _ROW_TYPES[dtype], kr, vr, heads, qr, qor, rope_base,
             _stream_of(dev) if stream is None else stream)
@@ -184,7 +185,7 @@ def paged_attention(cache: PagedCache, q, out, workspace, cu_new=None, scale: fl
     if cu_new is not None:
         _check_cu("dgen_paged_attention", cache, cu_new)
         cu = cu_new.data_ptr()
-    elif n % cache.batch:
+    elif cache.batch < 1 or n % cache.batch:
         _bad("dgen_paged_attention", "without cu_new every sequence has the same number of rows")
     if not 0 <= window < 1 << 31:
         _bad("dgen_paged_attention", "window: wants 0 (none) or a count of positions below 2^31")

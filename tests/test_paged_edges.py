@@ -60,3 +60,25 @@ def test_misaligned_counts_and_lse_are_refused():
     for at, status in ((A + 2, dg.DGEN_EINVAL), (A + 4, dg.DGEN_ESCRATCH)):
         assert dg._lib.dgen_paged_attention(ctypes.byref(_cache()), 2, None, 0, 4, r, r, 0.125, 1, 0, 0.0, at, A, 16,
                                             None) == status
+
+
+# ------------------------------------------------------------------ the binding's own checks
+
+def _binding_cache(batch=1):
+    """A handle as PagedCache makes it, for tensors that no GPU holds: every call here is refused before the C entry."""
+    cache = object.__new__(dg.paged.PagedCache)
+    cache._dev, cache._row_types, cache.head_dim, cache.batch, cache.n_kv_heads = -1, (torch.bfloat16,), 64, batch, 2
+    return cache
+
+
+def _refused(f, *args, **kw):
+    with pytest.raises(dg.DgenError) as e:
+        f(*args, **kw)
+    assert e.value.status == dg.DGEN_EINVAL
+
+
+@pytest.mark.parametrize("n", [0, 2])
+def test_a_batch_of_no_sequences_is_refused(n):
+    q, kv = (torch.zeros(n, h, 64, dtype=torch.bfloat16) for h in (4, 2))
+    _refused(dg.paged_attention, _binding_cache(0), q, q.clone(), torch.zeros(64, dtype=torch.uint8))
+    _refused(dg.paged_append, _binding_cache(0), kv, kv)
