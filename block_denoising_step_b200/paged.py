@@ -27,6 +27,11 @@ def _need(ok: bool, call: str, what: str) -> None:
         raise DgenError(call, DGEN_EINVAL, what)
 
 
+def _count(call: str, name: str, value: int) -> int:
+    _need(value < 1 << 31, call, f"{name}: {value} does not fit 32 bits")
+    return value
+
+
 class PagedCache:
     """One layer's cache: k, v [n_pages][n_kv_heads][page_size][head_dim] contiguous (bf16, fp16 or
     float8_e4m3fn), page_table [batch][pages] int32 (entries outside [0, n_pages) mean no page), kv_len
@@ -61,8 +66,10 @@ class PagedCache:
         _need(self.batch == 1 or stride == page_table.stride(0), call, "page_table's rows overlap")
         self._c = PagedCacheStruct(
             k.data_ptr(), v.data_ptr(), *(None if s is None else s.data_ptr() for s in (k_scale, v_scale)),
-            page_table.data_ptr(), kv_len.data_ptr(), _CACHE_TYPES[k.dtype], *k.shape[:3], k.shape[3], self.batch,
-            page_table.shape[1], stride)
+            page_table.data_ptr(), kv_len.data_ptr(), _CACHE_TYPES[k.dtype],
+            *(_count(call, n, x) for n, x in zip(("n_pages", "n_kv_heads", "page_size", "head_dim"), k.shape)),
+            _count(call, "batch", self.batch), _count(call, "table_pages", page_table.shape[1]),
+            _count(call, "table_stride", stride))
         self._ref = ctypes.addressof(self._c)
         self._dev = k.get_device()
         self._scale = 1.0 / math.sqrt(self.head_dim)
@@ -127,6 +134,8 @@ def paged_append(cache: PagedCache, k, v, q=None, q_out=None, cu_new=None, rope_
         _check_rows("dgen_paged_append", cache, "k", k, (shape[0] if len(shape) else 0, cache.n_kv_heads,
                                                          cache.head_dim), dtype)
     n = shape[0]
+    if n >> 31:
+        _bad("dgen_paged_append", "counts of rows are 32 bits")
     sv = v.stride()
     if v.shape != shape or sv[2] != 1 or v.dtype != dtype or v.get_device() != dev:
         _check_rows("dgen_paged_append", cache, "v", v, shape, dtype)
@@ -141,6 +150,8 @@ def paged_append(cache: PagedCache, k, v, q=None, q_out=None, cu_new=None, rope_
         if q_out.shape != qs or so[2] != 1 or q_out.dtype != dtype or q_out.get_device() != dev:
             _check_rows("dgen_paged_append", cache, "q_out", q_out, qs, dtype)
         heads = qs[1]
+        if heads >> 31:
+            _bad("dgen_paged_append", "counts of heads are 32 bits")
         qr, qor = _pack(q.data_ptr(), sq[0], sq[1]), _pack(q_out.data_ptr(), so[0], so[1])
     elif q_out is not None:
         _bad("dgen_paged_append", "q and q_out come together")
@@ -174,6 +185,8 @@ def paged_attention(cache: PagedCache, q, out, workspace, cu_new=None, scale: fl
     if out.shape != shape or so[2] != 1 or out.dtype != dtype or out.get_device() != dev:
         _check_rows("dgen_paged_attention", cache, "out", out, shape, dtype)
     n, heads = shape[0], shape[1]
+    if (n | heads) >> 31:
+        _bad("dgen_paged_attention", "counts of rows and heads are 32 bits")
     lse_at = None
     if lse is not None:
         if lse.shape != (n, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:

@@ -82,3 +82,23 @@ def test_a_batch_of_no_sequences_is_refused(n):
     q, kv = (torch.zeros(n, h, 64, dtype=torch.bfloat16) for h in (4, 2))
     _refused(dg.paged_attention, _binding_cache(0), q, q.clone(), torch.zeros(64, dtype=torch.uint8))
     _refused(dg.paged_append, _binding_cache(0), kv, kv)
+
+
+def test_counts_beyond_32_bits_are_refused():
+    """They would reach the C call as other counts (2^32 + 2 rows of one expanded token as 2)."""
+    for n, h in ((2 ** 32 + 2, 2), (2 ** 31, 2), (2, 2 ** 32 + 2)):
+        q = torch.zeros(1, 1, 64, dtype=torch.bfloat16).expand(n, h, 64)
+        _refused(dg.paged_attention, _binding_cache(), q, q, torch.zeros(64, dtype=torch.uint8))
+        if h == 2:
+            kv = torch.zeros(1, 1, 64, dtype=torch.bfloat16).expand(n, 2, 64)
+            _refused(dg.paged_append, _binding_cache(), kv, kv)
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16).expand(2, 2 ** 32 + 2, 64)
+    kv = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    _refused(dg.paged_append, _binding_cache(), kv, kv, q=q, q_out=q)
+
+
+def test_cache_counts_beyond_32_bits_are_refused():
+    """The struct's fields are 32 bits wide: a table row stride of 2^32 + 4 was kept as 4."""
+    for field, value in (("table_stride", 2 ** 32 + 4), ("n_pages", 2 ** 32 + 1), ("page_size", 2 ** 31)):
+        _refused(dg.paged._count, "PagedCache", field, value)
+    assert dg.paged._count("PagedCache", "page_size", 2 ** 31 - 1) == 2 ** 31 - 1
