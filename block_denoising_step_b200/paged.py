@@ -19,6 +19,7 @@ _append, _attention = _lib.dgen_paged_append, _lib.dgen_paged_attention
 _pack = struct.Struct("Qqq").pack
 _stream_of = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() without the object around it
 _ROW_TYPES = {torch.bfloat16: 0, torch.float16: 1}
+_SMALLEST = 2.0 ** -149  # fp32's: less would reach the C call as 0
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
 
@@ -161,6 +162,8 @@ def paged_append(cache: PagedCache, k, v, q=None, q_out=None, cu_new=None, rope_
         cu = cu_new.data_ptr()
     elif cache.batch < 1 or n % cache.batch:
         _bad("dgen_paged_append", "without cu_new every sequence has the same number of rows")
+    if 0.0 < rope_base < _SMALLEST:
+        _bad("dgen_paged_append", "rope_base: fp32 has no such number")
     args = (cache._ref, n, cu, _ROW_TYPES[dtype], kr, vr, heads, qr, qor, rope_base,
             _stream_of(dev) if stream is None else stream)
     if dev != torch.cuda.current_device():
@@ -202,6 +205,8 @@ def paged_attention(cache: PagedCache, q, out, workspace, cu_new=None, scale: fl
         _bad("dgen_paged_attention", "without cu_new every sequence has the same number of rows")
     if not 0 <= window < 1 << 31:
         _bad("dgen_paged_attention", "window: wants 0 (none) or a count of positions below 2^31")
+    if 0.0 < cap < _SMALLEST:
+        _bad("dgen_paged_attention", "cap: fp32 has no such number")
     args = (cache._ref, n, cu, _ROW_TYPES[dtype], heads, _pack(q.data_ptr(), st[0], st[1]),
             _pack(out.data_ptr(), so[0], so[1]), cache._scale if scale is None else scale, 1 if causal else 0, window,
             cap, lse_at, workspace.data_ptr(), workspace.numel(),

@@ -102,3 +102,11 @@ def test_cache_counts_beyond_32_bits_are_refused():
     for field, value in (("table_stride", 2 ** 32 + 4), ("n_pages", 2 ** 32 + 1), ("page_size", 2 ** 31)):
         _refused(dg.paged._count, "PagedCache", field, value)
     assert dg.paged._count("PagedCache", "page_size", 2 ** 31 - 1) == 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("tiny", [1e-60, 1e-46, 5e-324])
+def test_numbers_that_fp32_rounds_to_zero_are_refused(tiny):
+    """Zero means no cap and no rotation."""
+    q, kv = (torch.zeros(1, h, 64, dtype=torch.bfloat16) for h in (4, 2))
+    _refused(dg.paged_attention, _binding_cache(), q, q.clone(), torch.zeros(64, dtype=torch.uint8), cap=tiny)
+    _refused(dg.paged_append, _binding_cache(), kv, kv, rope_base=tiny)
