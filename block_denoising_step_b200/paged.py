@@ -87,6 +87,9 @@ def paged_workspace(device=None):
 def paged_synchronize(workspace, stream: int | None = None) -> None:
     """Wait for the stream; raises DgenError (EDEVICE) if a device-side bounded wait ran out in a call with this
     workspace since the last check."""
+    _need(workspace.is_cuda and workspace.dtype == torch.uint8 and workspace.is_contiguous() and
+          workspace.numel() >= _lib.dgen_paged_workspace_bytes(), "dgen_paged_synchronize",
+          "workspace: wants a paged_workspace()")
     st = torch.cuda.current_stream(workspace.device).cuda_stream if stream is None else stream
     _off_device("dgen_paged_synchronize", workspace.device, workspace.data_ptr(), st)
 

@@ -180,6 +180,15 @@ def test_nothing_is_joined_after_a_wait_ran_out():
     assert torch.equal(out, good)
 
 
+def test_synchronize_refuses_part_of_a_workspace():
+    ws = dg.paged_workspace()
+    for part in (ws[:64], ws[16:], ws[:: 2]):
+        with pytest.raises(dg.DgenError) as e:
+            dg.paged_synchronize(part)
+        assert e.value.status == dg.DGEN_EINVAL
+    dg.paged_synchronize(ws)
+
+
 # ------------------------------------------------------------------ the append's division
 
 # powers of two and thirds of them (ties with many rows), both sides of 2^-100 and 2^100, the ends of fp32's range

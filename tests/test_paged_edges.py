@@ -110,3 +110,9 @@ def test_numbers_that_fp32_rounds_to_zero_are_refused(tiny):
     q, kv = (torch.zeros(1, h, 64, dtype=torch.bfloat16) for h in (4, 2))
     _refused(dg.paged_attention, _binding_cache(), q, q.clone(), torch.zeros(64, dtype=torch.uint8), cap=tiny)
     _refused(dg.paged_append, _binding_cache(), kv, kv, rope_base=tiny)
+
+
+def test_synchronize_refuses_what_is_no_workspace():
+    """The call reads and writes the workspace's head whatever the tensor's size."""
+    for ws in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(16, dtype=torch.uint8), torch.zeros(1 << 20)):
+        _refused(dg.paged_synchronize, ws)
