@@ -13,7 +13,7 @@
 // frequencies once and its tokens' sines once, for all heads.
 //
 // Memory-bound: every row is read and written once, 16 bytes per access.  A
-// block takes up to kTokens tokens (one warp each finds its token's sequence
+// block takes up to kAppendTokens tokens (one warp each finds its token's sequence
 // and page), then all threads sweep (row, 8 + 8 elements) items.  A thread's next
 // items are on their way while it writes the current ones, the first ones already
 // while the pages are looked up, which their addresses do not need.
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kAppendThreads, E4M3 ? 3 : 4) paged_append_ker
     constexpr int STEP = kAppendThreads / CH;  // rows between a thread's items
     constexpr int U = 2;                       // items in flight besides the ones at hand
     __shared__ double freq[HALF];
-    __shared__ float2 cs[kAppendTokens][HALF];
+    __shared__ __align__(16) float2 cs[kAppendTokens][HALF];  // (read 16 bytes at a time)
     __shared__ int s_pos[kAppendTokens], s_page[kAppendTokens], s_off[kAppendTokens];
     using H2 = Half2<BF>;
     pdl_enter();
