@@ -26,6 +26,7 @@ constexpr size_t kHeadBytes = kCounterBytes + kMaxGrid * 64;             // and 
 static_assert(sizeof(paged::Piece) <= 64, "join list");
 constexpr int kMaxDevices = 64;
 constexpr int kMaxHeads = 65536;         // query or KV heads: a token's rows and items count in 32 bits
+constexpr int kMaxSms = 148;             // SMs that an attention launch uses at most (its workspace)
 constexpr int kMaxSplitCtas = 4;         // CTAs per SM of the split kernel at most
 
 int sm_count(int dev) {
@@ -351,7 +352,7 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (workspace_bytes < static_cast<int64_t>(kHeadBytes)) return DGEN_ESCRATCH;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DGEN_ECUDA;
-    const int sms = sm_count(dev);
+    const int sms = std::min(sm_count(dev), kMaxSms);
     if (sms < 1) return DGEN_ECUDA;
     paged::AttendArgs a{};
     a.c = view(cache, n_tokens, cu);
@@ -409,8 +410,8 @@ int dgen_paged_attention(const dgen_paged_cache* cache, int32_t n_tokens, const 
 }
 
 int64_t dgen_paged_workspace_bytes(void) {
-    // two partial results per CTA of the largest launch (148 CTAs, 128 rows x (256 + 2) floats each)
-    return static_cast<int64_t>(kHeadBytes) + int64_t{2} * 148 * paged::kBlkRows * 258 * 4;
+    // two partial results per CTA of the largest launch (128 rows x (256 + 2) floats each)
+    return static_cast<int64_t>(kHeadBytes) + int64_t{2} * kMaxSms * paged::kBlkRows * 258 * 4;
 }
 
 int dgen_paged_synchronize(void* workspace, void* stream) {
