@@ -370,7 +370,6 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     // scores below 2^-100 weigh alike, and those that 2^126 bends are so far apart that one key takes all.
     a.cap = cap > 0.f ? std::clamp(cap, 0x1p-100f, 0x1p126f) : 0.f;
     a.q_bf16 = type == DGEN_TYPE_BF16;
-    a.min_blocks = 1;
     Workspace ws{static_cast<unsigned int*>(workspace), static_cast<int*>(workspace) + kMaxGrid,
                  reinterpret_cast<paged::Piece*>(static_cast<uint8_t*>(workspace) + kCounterBytes),
                  reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeadBytes),

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(BlockLayout<HD>::THREADS, 1)
 
     if (warp == 2) {
         Walk walk;
-        walk.start(c, a.p, lane, a.min_blocks, blockIdx.x, a.n_ctas);
+        walk.start(c, a.p, lane, blockIdx.x, a.n_ctas);
         // What the join kernel has to know of the unit that starts here and goes on behind: none until it is met, so
         // that a walk that a wait ends early leaves no record of an earlier call.
         if (lane == 0) a.joins[blockIdx.x].end = 1;

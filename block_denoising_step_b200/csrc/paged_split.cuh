@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32, SplitLayout<HD, ES, NT>::CTA
 
     if (warp == 0) {
         Walk walk;
-        walk.start(c, a.p, lane, a.min_blocks, blockIdx.x, a.n_ctas);
+        walk.start(c, a.p, lane, blockIdx.x, a.n_ctas);
         reinterpret_cast<Walk*>(smem + S::WALK_OFF)[lane] = walk;
         walk_on(0);
     }

@@ -194,8 +194,7 @@ struct Walk {
     int member, cut;  // cut > 0: the line is made of pieces of `cut` blocks, which no unit shares
     int total, per, t, t_end;
 
-    __device__ __forceinline__ void start(const CacheView& c, const Partition& p, int lane, int min_blocks, int cta,
-                                          int n_ctas) {
+    __device__ __forceinline__ void start(const CacheView& c, const Partition& p, int lane, int cta, int n_ctas) {
         const int log2_ts = __ffs(p.TS) - 1, teams = n_ctas >> log2_ts;  // (TS is a power of two)
         member = cta & (p.TS - 1);
         int before = 0, units = 0, most = 0, nominal = 0;  // most: blocks of the longest unit, at most
@@ -218,7 +217,6 @@ struct Walk {
             // others pieces of T / (teams - units), of which there are at most T / that + units = teams.
             cut = nominal == units * most ? (most + teams / units - 1) / (teams / units)
                                           : (nominal + teams - units - 1) / (teams - units);
-            if (cut < min_blocks) cut = min_blocks;
             if (most <= cut + kWholeSlack) cut = most;
         } else if (units > 0 && static_cast<long long>((units + teams - 1) / teams) * most <= per + kWholeSlack) {
             cut = most;  // whole units
@@ -233,8 +231,6 @@ struct Walk {
             }
             total = before;
             per = (total + teams - 1) / teams;
-        } else if (per < min_blocks) {
-            per = min_blocks;
         }
         // (per * team can pass 2^31 only behind the line's end)
         const long long at = static_cast<long long>(per) * (cta >> log2_ts);
@@ -334,8 +330,6 @@ struct Walk {
     }
 };
 
-struct Piece;
-
 struct AttendArgs {
     CacheView c;
     RowsView q, out;
@@ -347,7 +341,7 @@ struct AttendArgs {
     unsigned int* counters;  // [grid]
     Piece* joins;            // [grid], block kernel
     float* parts;            // [2 n_ctas][R][HD] then [2 n_ctas][R][2]
-    int min_blocks, n_ctas;
+    int n_ctas;
 };
 
 // Capped scores, log2(e) cap tanh(s / cap), from x = log2(e) s and u = s / cap.
