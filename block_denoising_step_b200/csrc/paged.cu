@@ -24,6 +24,7 @@ constexpr int kMaxGrid = 1023;           // CTAs of an attention launch at most 
 constexpr size_t kCounterBytes = (kMaxGrid + 1) * sizeof(unsigned int);  // and the device-side error word
 constexpr size_t kHeadBytes = kCounterBytes + kMaxGrid * 64;             // and the block kernel's join list
 static_assert(sizeof(paged::Piece) <= 64, "join list");
+constexpr int kMaxLine = INT32_MAX - kMaxGrid;  // blocks of all units: rounded up to the grid they count in 32 bits
 constexpr int kMaxDevices = 64;
 constexpr int kMaxHeads = 65536;         // query or KV heads: a token's rows and items count in 32 bits
 constexpr int kMaxSms = 148;             // SMs that an attention launch uses at most (its workspace)
@@ -159,7 +160,7 @@ int launch_split(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     const int64_t rows = static_cast<int64_t>(a.c.n_tokens) * a.p.G;
     const int64_t tiles = std::min<int64_t>(rows, rows / a.p.R + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + a.p.KB - 1) / a.p.KB;
-    if (tiles * (blocks + 3) >= INT32_MAX) return DGEN_EINVAL;  // (rows <= 2^31, blocks <= 2^24: no overflow)
+    if (tiles * (blocks + 3) >= kMaxLine) return DGEN_EINVAL;  // (rows <= 2^31, blocks <= 2^24: no overflow)
     grid = std::max<int64_t>(1, std::min(grid, tiles * blocks));
     if (2 * static_cast<size_t>(grid) * S::R * (HD + 2) > ws.floats) return DGEN_ESCRATCH;
     a.counters = ws.counters;
@@ -250,7 +251,7 @@ int launch_block(cudaStream_t st, int dev, int sms, paged::AttendArgs a, const W
     a.p.unit_cost = 4;
     const int64_t units = std::min<int64_t>(rows, rows / (a.p.R * a.p.TS) + a.c.B) * a.c.Hkv;
     const int64_t blocks = (static_cast<int64_t>(a.c.table_pages) * a.c.page + 2 * paged::kBlkKeys - 2) / paged::kBlkKeys;
-    if (units * (blocks + 4) >= INT32_MAX) return DGEN_EINVAL;
+    if (units * (blocks + 4) >= kMaxLine) return DGEN_EINVAL;
     const int64_t teams = std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid) / a.p.TS, units * blocks));
     const int64_t grid = teams * a.p.TS;
     if (2 * static_cast<size_t>(grid) * paged::kBlkRows * (HD + 2) > ws.floats) return DGEN_ESCRATCH;

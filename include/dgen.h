@@ -481,7 +481,7 @@ int dgen_sample_from_logits_noalloc(const float* logits_dev, int32_t* tok_dev, u
  * values: value = scale * stored (stored = value / scale, round to nearest even,
  * saturating).  head_dim 64, 128 or 256; any n_q_heads / n_kv_heads ratio.
  * Attention also wants (row tiles of 8 or more query rows) x (64-key blocks of a
- * table row's capacity) below 2^31.
+ * table row's capacity) below 2^31 - 1024.
  * Errors: EINVAL (shape, type, alignment), ESCRATCH (workspace too small),
  * ECUDA.  stream: a cudaStream_t of the current device; asynchronous, no
  * allocation, no synchronisation; may be captured into a graph. */
