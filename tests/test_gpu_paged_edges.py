@@ -216,3 +216,64 @@ def test_e4m3_values_are_the_divisions_to_the_bit(t):
         nan = want.float().isnan()
         assert torch.equal(got.cpu()[:, :, 0].float().isnan(), nan)
         assert (same | nan).all(), [(SCALES[h], int((~same & ~nan)[:, h].sum())) for h in range(hkv)]
+
+
+# ------------------------------------------------------------------ batches and contexts as they are used
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("hd,group,new", [(256, 2, 256), (256, 2, 250), (128, 4, 120), (64, 8, 64), (128, 3, 83), (64, 1, 255)])
+@pytest.mark.parametrize("masks", [dict(causal=False), dict(causal=True), dict(causal=True, window=300),
+                                   dict(causal=False, window=100, cap=20.0)], ids=["all", "causal", "window", "capped"])
+def test_canvases_over_prompts_of_unequal_length(kind, hd, group, new, masks, workspace):
+    """As many new tokens in every sequence and no cu_new: neighbouring row tiles go to teams of CTAs (two to four)."""
+    lens = [new + p for p in (2048, 44, 0, 855, 1, 300)]
+    cache = make_cache(kind, lens, 2, hd, 16, seed=170)
+    cache.page_table[3, 5:9] = -1
+    q = (2 * torch.randn(new * len(lens), 2 * group, hd, generator=_gen(171), device="cuda")).to(TYPES[kind][0])
+    check(cache, q, [new] * len(lens), workspace, uniform=True, **masks)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16-e4m3"])
+@pytest.mark.parametrize("new", [1, 20])
+def test_batches_of_more_sequences_than_a_warp_has_lanes(kind, new, workspace):
+    """Two chunks of lengths and a bit, some sequences empty in between."""
+    g = torch.Generator().manual_seed(180)
+    lens = torch.randint(new, 400, (71,), generator=g).tolist()
+    cache = make_cache(kind, lens, 1, 64, 16, seed=181)
+    q = (2 * torch.randn(71 * new, 4, 64, generator=_gen(182), device="cuda")).to(TYPES[kind][0])
+    check(cache, q, [new] * 71, workspace, uniform=True, causal=True)
+    counts = [new if i % 3 else 0 for i in range(71)]
+    check(cache, q[:sum(counts)], counts, workspace, causal=True, window=77)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("hd,group,new,length", [(128, 8, 1, 40000), (256, 2, 1, 40000), (64, 12, 1, 40000),
+                                                 (128, 4, 1, 131071), (128, 2, 64, 40000), (256, 2, 130, 20000)])
+def test_long_contexts(kind, hd, group, new, length, workspace):
+    """Beside the bound of every output, whose sums of tens of thousands of weights are counted at their worst: the
+    root of the mean square.  A rounding spreads evenly over a step, so the output's leaves 1/sqrt(3) of the half
+    step, and the weights' independent ones 1/sqrt(3) of theirs times the root of sum p^2 v^2; a quarter is left for the
+    scores' errors, a few 2^-24 of scores of about ten."""
+    cache = make_cache(kind, [length], 1, hd, 64, seed=190)
+    q = (2 * torch.randn(new, group, hd, generator=_gen(191), device="cuda")).to(TYPES[kind][0])
+    out, _ = check(cache, q, [new], workspace, uniform=True, causal=True)
+    step, half = bounds.p_step(cache, q, new * group)
+    want = bounds.attention(cache, q, [new], p_step=step, p_half=half)[0]
+    rounding = (ref.half_step(q.dtype, want) / 3 ** 0.5).square().mean().sqrt()
+    spread = step / 3 ** 0.5 * weights_spread(cache, q, new)
+    assert (out.double() - want).square().mean().sqrt() <= 1.25 * (rounding ** 2 + spread ** 2).sqrt()
+
+
+def weights_spread(cache, q, new):
+    """Root of the mean over outputs of sum p^2 v^2, for one sequence of one KV head."""
+    n_pages, _, page, hd = cache.k.shape
+    total = int(cache.kv_len[0])
+    j = torch.arange(total)
+    ids = cache.page_table[0].cpu()[j // page].long().cuda()
+    k, v = cache.k[ids, 0, (j % page).cuda()].double(), cache.v[ids, 0, (j % page).cuda()].double()
+    if cache.k_scale is not None:
+        k, v = k * cache.k_scale[0].double(), v * cache.v_scale[0].double()
+    s = torch.einsum("nhd,ld->nhl", q.double(), k) / math.sqrt(hd)
+    p = torch.arange(total - new, total, device="cuda")
+    s = s.masked_fill((torch.arange(total, device="cuda") > p[:, None])[:, None], -math.inf)
+    return (torch.softmax(s, -1).square() @ v.square()).mean().sqrt()

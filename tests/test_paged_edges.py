@@ -1,10 +1,13 @@
 """The paged cache's calls at the edges of what they allow, what needs no GPU."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
 
 import block_denoising_step_b200 as dg
+from block_denoising_step_b200 import build
 from tests.test_paged import A, _append, _attend, _cache, _rows
 
 
@@ -116,3 +119,17 @@ def test_synchronize_refuses_what_is_no_workspace():
     """The call reads and writes the workspace's head whatever the tensor's size."""
     for ws in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(16, dtype=torch.uint8), torch.zeros(1 << 20)):
         _refused(dg.paged_synchronize, ws)
+
+
+# ------------------------------------------------------------------ the division of a batch
+
+def test_closed_forms_of_the_unit_walk(tmp_path):
+    """Host code of csrc/paged_work.cuh, compiled with a check that sums block by block."""
+    if not os.path.exists(build.NVCC):
+        pytest.skip("needs nvcc")
+    exe = str(tmp_path / "check")
+    subprocess.check_call([build.NVCC, "-std=c++17", "-O1", "--expt-relaxed-constexpr", "-gencode",
+                           "arch=compute_100a,code=sm_100a", "-I", build.SRC_DIR, "-o", exe,
+                           os.path.join(os.path.dirname(os.path.abspath(__file__)), "paged_units_check.cu")])
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout
