@@ -277,3 +277,157 @@ def weights_spread(cache, q, new):
     p = torch.arange(total - new, total, device="cuda")
     s = s.masked_fill((torch.arange(total, device="cuda") > p[:, None])[:, None], -math.inf)
     return (torch.softmax(s, -1).square() @ v.square()).mean().sqrt()
+
+
+# ------------------------------------------------------------------ layouts
+
+@pytest.mark.parametrize("page", [8, 24, 40, 48, 96, 200, 384, 1024])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_many_rows_over_pages_of_any_size_that_8_divides(page, hd, workspace):
+    lens, new = [900, 129, 41, 1030], [200, 64, 41, 30]
+    cache = make_cache("bf16", lens, 2, hd, page, seed=200)
+    q = (2 * torch.randn(sum(new), 6, hd, generator=_gen(201), device="cuda")).bfloat16()
+    check(cache, q, new, workspace, causal=True)
+    check(cache, q, new, workspace, causal=False, window=130, cap=15.0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16-e4m3"])
+@pytest.mark.parametrize("group", [100, 127, 128, 129, 200])
+def test_large_groups(kind, group, workspace):
+    lens, new = [300, 77, 64], [5, 1, 2]
+    cache = make_cache(kind, lens, 1, 128, 16, seed=210)
+    q = (2 * torch.randn(sum(new), group, 128, generator=_gen(211), device="cuda")).to(TYPES[kind][0])
+    check(cache, q, new, workspace, causal=True)
+    check(cache, q, new, workspace, causal=False, window=40)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16-e4m3"])
+@pytest.mark.parametrize("new", [1, 70])
+def test_any_order_of_strides(kind, new, workspace):
+    """Rows stored by head, one row for every token, one head for all, tables and lse inside larger ones, in place."""
+    t, lens = TYPES[kind][0], [300, 80]
+    cache = make_cache(kind, lens, 2, 64, 16, seed=220)
+    n = 2 * new
+    wide = torch.full((2, 40), -7, dtype=torch.int32, device="cuda")
+    wide[:, 3:3 + cache.page_table.shape[1]] = cache.page_table
+    cache = dg.PagedCache(cache.k, cache.v, wide[:, 3:3 + cache.page_table.shape[1]], cache.kv_len, cache.k_scale,
+                          cache.v_scale)
+    rows = torch.randn(n, 4, 64, generator=_gen(221), device="cuda").to(t)
+    by_head = rows.transpose(0, 1).contiguous().transpose(0, 1)
+    for q in (by_head, rows[:1].expand(n, 4, 64), rows[:, :1].expand(n, 4, 64)):
+        want = torch.empty_like(rows)
+        dg.paged_attention(cache, q.contiguous(), want, workspace, causal=False)
+        out = torch.empty(4, n, 64, dtype=t, device="cuda").transpose(0, 1)
+        dg.paged_attention(cache, q, out, workspace, causal=False)
+        step = bounds.p_step(cache, q, 2 * new)
+        exact, _, bound, _ = bounds.attention(cache, q, [new, new], causal=False, p_step=step[0], p_half=step[1])
+        for x in (want, out):
+            assert ((x.double() - exact).abs() <= ref.half_step(t, exact) * (1 + 2.0 ** -7) + bound).all()
+    x = rows.clone()
+    dg.paged_attention(cache, x, x, workspace, causal=False)
+    dg.paged_attention(cache, rows, want, workspace, causal=False)
+    assert torch.equal(x, want)
+
+
+def test_pages_shared_by_sequences(workspace):
+    """A common prompt's pages in every table, each sequence's own behind them."""
+    cache = make_cache("bf16", [160] * 5, 2, 128, 16, seed=230)
+    cache.page_table[:, :8] = cache.page_table[0, :8].clone()
+    cache.kv_len.copy_(torch.tensor([160, 140, 129, 150, 128]))
+    for new in (1, 40):
+        q = (2 * torch.randn(5 * new, 8, 128, generator=_gen(231), device="cuda")).bfloat16()
+        check(cache, q, [new] * 5, workspace, uniform=True, causal=True)
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_16_bit_pools_beyond_32_bit_offsets(new, workspace):
+    page, hd = 64, 128
+    n_pages = (1 << 32) // (page * hd) + 8
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    k = torch.empty(n_pages, 1, page, hd, dtype=torch.float16, device="cuda")
+    v = torch.empty_like(k)
+    used = [n_pages - 1, 5, n_pages - 7, n_pages // 2 + 3]
+    g = _gen(240)
+    for x in (k, v):
+        for i in used:
+            x[i] = torch.randn(1, page, hd, generator=g, device="cuda").half()
+    cache = dg.PagedCache(k, v, torch.tensor([used], dtype=torch.int32, device="cuda"),
+                          torch.tensor([250], dtype=torch.int32, device="cuda"))
+    rows = torch.randn(new, 6, hd, generator=g, device="cuda").half()
+    dg.paged_append(cache, rows[:, 4:5], rows[:, 5:])
+    at = torch.arange(250 - new, 250, device="cuda")
+    ids = torch.tensor(used, device="cuda")[at // page]
+    assert torch.equal(k[ids, 0, at % page], rows[:, 4]) and torch.equal(v[ids, 0, at % page], rows[:, 5])
+    check(cache, rows[:, :4], [new], workspace)
+
+
+# ------------------------------------------------------------------ captured calls
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_captured_batches_follow_counts_lengths_and_pages(cap, workspace):
+    """One graph of append and attention for a ragged batch: replays with other counts, lengths and tables, from one
+    token each to one sequence with all of them, on a workspace that other calls use in between."""
+    b, n, hq, hkv = 4, 120, 6, 2
+    cache = make_cache("bf16", [1200] * b, hkv, 128, 16, seed=250)
+    cache.k.nan_to_num_(0.0), cache.v.nan_to_num_(0.0)
+    g = _gen(251)
+    rows = torch.randn(n, hq + 2 * hkv, 128, generator=g, device="cuda").bfloat16()
+    q, k, v = rows.split([hq, hkv, hkv], dim=1)
+    qr, out = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty(n, hq, 128, device="cuda").bfloat16()
+    lse, cu = torch.empty(n, hq, device="cuda"), cu_of([30] * b)
+
+    def step():
+        dg.paged_append(cache, k, v, q=q, q_out=qr, cu_new=cu, rope_base=10000.0)
+        dg.paged_attention(cache, qr, out, workspace, cu_new=cu, cap=cap, lse=lse)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new, lens in (([30, 30, 30, 30], [1200, 31, 30, 700]), ([1, 1, 1, 1], [900, 1, 17, 16]),
+                      ([0, 120, 0, 0], [5, 1000, 0, 3]), ([0, 0, 0, 0], [1, 2, 3, 4]), ([2, 100, 3, 10], [2, 1111, 64, 640])):
+        cu.copy_(cu_of(new))
+        cache.kv_len.copy_(torch.tensor(lens))
+        cache.page_table.copy_(cache.page_table.roll(1, 0))
+        rows.normal_(generator=g)
+        out.fill_(7.0), lse.fill_(7.0), qr.fill_(1.0)
+        graph.replay()
+        dg.paged_synchronize(workspace)
+        got, m = out.clone(), sum(new)
+        assert (got[m:] == 7.0).all() and (lse[m:] == 7.0).all()
+        if m:
+            step_, half = max((bounds.p_step(cache, q, c * hq // hkv) for c in new if c))
+            want, want_lse, bound, lse_bound = bounds.attention(cache, qr, new, cap=cap, p_step=step_, p_half=half)
+            assert ((got.double() - want).abs() <= ref.half_step(q.dtype, want) * (1 + 2.0 ** -7) + bound)[:m].all()
+            assert ((lse.double() - want_lse).abs() <= lse_bound)[:m].all()
+        dg.paged_attention(cache, qr, out, workspace, cu_new=cu_of([30] * b), causal=False)  # the graph's own next to come
+
+
+def test_two_graphs_at_once_with_a_workspace_each():
+    caches = [make_cache("bf16", [2304], 2, 128, 16, seed=260 + i) for i in range(2)]
+    spaces = [dg.paged_workspace() for _ in range(2)]
+    qs = [torch.randn(256, 4, 128, generator=_gen(262 + i), device="cuda").bfloat16() for i in range(2)]
+    outs, first = [torch.empty_like(x) for x in qs], []
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        dg.paged_attention(caches[i], qs[i], outs[i], spaces[i], causal=False)
+        first.append(outs[i].clone())
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graphs[i]):
+            for _ in range(4):
+                dg.paged_attention(caches[i], qs[i], outs[i], spaces[i], causal=False)
+        outs[i].zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        dg.paged_synchronize(spaces[i])
+        assert torch.equal(outs[i], first[i])
