@@ -49,31 +49,31 @@ def attention(cache, q, new, *, scale=None, causal=True, window=0, cap=0.0, p_st
             kh, vh = cache.k[ids, h, j % page].double(), cache.v[ids, h, j % page].double()
             if cache.k_scale is not None:
                 kh, vh = kh * cache.k_scale[h].double(), vh * cache.v_scale[h].double()
-            for head in range(h * g, (h + 1) * g):
-                qh = q[rows, head].double()
-                s = qh @ kh.T * scale
-                off = qh.abs() @ kh.abs().T * (scale * hd * 2.0 ** -24)
-                if cache.k_scale is not None:
-                    off += qh.abs().amax(1)[:, None] * kh.abs().sum(1) * (scale * 2.0 ** -39)
-                if cap:
-                    s = cap * torch.tanh(s / cap)
-                    small = bool((s.abs() <= 0.5 * cap)[see].all())
-                    off += s.abs() * (1.6e-7 + 5 * 2.0 ** -24) if small else torch.full_like(s, 6 * 2.0 ** -24 * cap)
-                s = s.masked_fill(~see, -math.inf)
-                top = torch.where(live, s.amax(1), 0.0)
-                off += torch.where(see, s, 0.0).abs() * 2.0 ** -22 + top.abs()[:, None] * 2.0 ** -22
-                worst = torch.where(see, off, 0.0).amax(1)
-                e = torch.exp(s - top[:, None])
-                tot = e.sum(1)
-                pr = e / tot.clamp_min(1e-300)[:, None]
-                out[rows, head] = pr @ vh
-                lse[rows, head] = torch.where(live, top + torch.log(tot), -math.inf)
-                c = 2 * worst + p_step + 2.0 ** -22 + (count + 16) * 2.0 ** -24
-                bound[rows, head] = (pr @ vh.abs()) * c[:, None]
-                if p_half:
-                    bound[rows, head] += (count / tot.clamp_min(1.0) * 2.0 ** -32)[:, None] * vh.abs().amax()
-                lse_bound[rows, head] = 2 * worst + (count + 16) * 2.0 ** -24 + torch.where(
-                    live, lse[rows, head].abs(), 0.0) * 2.0 ** -22 + 2.0 ** -22
+            heads = slice(h * g, (h + 1) * g)
+            qh, seen = q[rows, heads].double().transpose(0, 1), see[None]  # [group][n][hd]
+            s = qh @ kh.T * scale
+            off = qh.abs() @ kh.abs().T * (scale * hd * 2.0 ** -24)
+            if cache.k_scale is not None:
+                off += qh.abs().amax(-1, keepdim=True) * kh.abs().sum(1) * (scale * 2.0 ** -39)
+            if cap:
+                s = cap * torch.tanh(s / cap)
+                small = bool((s.abs() <= 0.5 * cap)[seen.expand_as(s)].all())
+                off += s.abs() * (1.6e-7 + 5 * 2.0 ** -24) if small else 6 * 2.0 ** -24 * cap
+            s = s.masked_fill(~seen, -math.inf)
+            top = torch.where(live, s.amax(-1), 0.0)
+            off += torch.where(seen, s, 0.0).abs() * 2.0 ** -22 + top.abs()[..., None] * 2.0 ** -22
+            worst = torch.where(seen, off, 0.0).amax(-1)
+            e = torch.exp(s - top[..., None])
+            tot = e.sum(-1)
+            pr = e / tot.clamp_min(1e-300)[..., None]
+            log_sum = torch.where(live, top + torch.log(tot), -math.inf)
+            c = 2 * worst + p_step + 2.0 ** -22 + (count + 16) * 2.0 ** -24
+            far = (pr @ vh.abs()) * c[..., None]
+            if p_half:
+                far += (count / tot.clamp_min(1.0) * 2.0 ** -32)[..., None] * vh.abs().amax()
+            far_lse = 2 * worst + (count + 16) * 2.0 ** -24 + torch.where(live, log_sum.abs(), 0.0) * 2.0 ** -22 + 2.0 ** -22
+            for to, x in ((out, pr @ vh), (lse, log_sum), (bound, far), (lse_bound, far_lse)):
+                to[rows, heads] = x.transpose(0, 1)
     return out, lse, bound, lse_bound
 
 
