@@ -191,10 +191,12 @@ int split_hd(cudaStream_t st, int dev, int sms, const paged::AttendArgs& a, cons
 }
 
 // Rows per KV head of one sequence above which the tcgen05 kernel takes it, although its tiles hold 128: it
-// reads the keys once for all of them.  Split kernel / tcgen05 kernel in us, 8 KV heads, lengths of 4,352 keys in
-// 16 sequences (and one of 301): hd 128, 8 rows 51 / 50 (9.8 / 11.1), 16 rows 57 / 51 (13.9 / 11.1), 24 rows
-// 100 / 52; hd 256, 8 rows 99 / 91 (12.9 / 15.5), 16 rows 111 / 94 (19.7 / 15.5), 24 rows 195 / 94; hd 64, whose
-// short rows the split kernel streams with more warps, 16 rows 37 / 43 (10.7 / 14.0), 24 rows 53 / 42 (14.0 / 14.1).
+// reads the keys once for all of them (and rounds each weight once, where the split kernel keeps about 16 bits).
+// Split kernel / tcgen05 kernel in us, 8 KV heads, lengths of 4,352 keys in 16 sequences (and one of 301):
+// hd 128, 8 rows 51 / 50 (9.8 / 11.1), 16 rows 57 / 51 (13.9 / 11.1), 24 rows 100 / 52; hd 256, 8 rows 99 / 91
+// (12.9 / 15.5), 16 rows 111 / 94 (19.7 / 15.5), 24 rows 195 / 94; hd 64, whose short rows the split kernel
+// streams with more warps, 16 rows 37 / 43 (10.7 / 14.0), 24 rows 53 / 42 (14.0 / 14.1).  No count serves every
+// length at hd 64: 64 sequences of 16 rows over 8,192 keys take 101 / 149, one of 12 rows over 40,000 45 / 33.
 constexpr int block_min_rows(int hd) { return hd >= 128 ? 8 : 16; }
 
 // Whether the tcgen05 kernel can take this call's long sequences: 16-bit cache, a

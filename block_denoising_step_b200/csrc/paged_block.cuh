@@ -33,13 +33,14 @@
 // output's own rounding where few do.
 //
 // Measured on a B200 (device time of a replayed graph): eight canvases of 256 tokens over
-// 4,352 keys, 16 heads on 8 of 256, 128 us (1,137 TFLOP/s; tensor cores); one over 2,304 keys
-// 24 us (five blocks per CTA: start-up and join outweigh them); six ragged causal chunks of up
-// to 1,024 tokens over 5,000 keys, 32 heads on 8 of 128, capped scores, 277 to 303 us (the
-// capped scores' fp32 work).
+// 4,352 keys, 16 heads on 8 of 256, 128 to 131 us on several boxes (1,117 to 1,139 TFLOP/s;
+// tensor cores); one over 2,304 keys 24.5 us (five blocks per CTA: start-up and join outweigh
+// them); six ragged causal chunks of up to 1,024 tokens over 5,000 keys, 32 heads on 8 of 128,
+// capped scores, 278 to 315 us (the capped scores' fp32 work; 470 with scores past the cap).
 //
-// Keys behind the sequence's end and absent pages are not loaded; scores there
-// are replaced by -inf, and the V rows are zeros (shared memory may hold anything).  Every wait is bounded; on a timeout the kernel records an
+// Pages behind the sequence's end and absent ones are not loaded; the last page part is, as
+// a whole.  Scores of keys that do not count are replaced by -inf, and their V rows by zeros
+// (shared memory may hold anything).  Every wait is bounded; on a timeout the kernel records an
 // error, drains its own copies and MMAs, frees its tensor memory and exits.
 #pragma once
 

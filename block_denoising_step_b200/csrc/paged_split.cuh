@@ -12,7 +12,7 @@
 // S^T's accumulator layout transposed 8 x 8 (movmatrix).  P is kept as hi + lo
 // 16-bit parts (about 16 significant bits, fp16's down to 2^-16 of the largest weight), so the
 // output's own rounding is the only one that shows; with an E4M3 cache and bf16 rows fp16's 11
-// bits alone do (2^-12 of a weight against the output's 2^-9).
+// bits alone do (2^-11 of a weight against the output's 2^-8).
 //
 // Memory-bound: every visible K and V row is read once.  Each warp streams its
 // own tiles of 16 or 32 keys through a private ring of shared memory (cp.async 16 bytes,
@@ -27,10 +27,10 @@
 // bytes, so the k order within 16 elements is permuted alike in K and Q.
 //
 // Measured on a B200 (device time of a replayed graph): 131,071 keys of 8 heads x 128 for
-// one token 89 us (6.05 TB/s); 64 tokens over up to 8,192 keys of 8 x 256 323 us (6.9 TB/s);
-// 48 tokens over up to 16,384 E4M3 keys of 8 x 128 189 us (4.4 TB/s: the conversions bound it);
+// one token 89 us (6.0 TB/s); 64 tokens over up to 8,192 keys of 8 x 256 326 us (6.8 TB/s);
+// 48 tokens over up to 16,384 E4M3 keys of 8 x 128 188 to 191 us (4.3 TB/s: the conversions bound it);
 // 128 tokens in windows of 1,024 keys of 12 x 64 74 us (4.8 TB/s: the start and end of short
-// units); one token over 301 keys 8.8 us (the chain of dependent loads and the join).
+// units); one token over 301 keys 8.9 us (the chain of dependent loads and the join).
 #pragma once
 
 #include "mma_sync.cuh"

@@ -78,15 +78,16 @@ class PagedCache:
 
 
 def paged_workspace(device=None):
-    """A zeroed workspace for paged_attention on `device` (default: the current one).  Calls that can overlap
-    on the GPU (other streams, replays of captured graphs) each need one of their own."""
+    """A workspace for paged_attention on `device` (default: the current one), zeroed on its current stream: a
+    call on another stream waits for that first.  Calls that can overlap on the GPU (other streams, replays of
+    captured graphs) each need one of their own."""
     return torch.zeros(_lib.dgen_paged_workspace_bytes(), dtype=torch.uint8,
                        device="cuda" if device is None else device)
 
 
 def paged_synchronize(workspace, stream: int | None = None) -> None:
     """Wait for the stream; raises DgenError (EDEVICE) if a device-side bounded wait ran out in a call with this
-    workspace since the last check."""
+    workspace (a paged_workspace()) since the last check: outputs since then are not valid."""
     _need(workspace.is_cuda and workspace.dtype == torch.uint8 and workspace.is_contiguous() and
           workspace.numel() >= _lib.dgen_paged_workspace_bytes(), "dgen_paged_synchronize",
           "workspace: wants a paged_workspace()")
