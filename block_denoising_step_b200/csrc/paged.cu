@@ -347,7 +347,7 @@ int attend(const dgen_paged_cache* cache, int32_t n_tokens, const int32_t* cu, i
     if (cache->type != DGEN_TYPE_E4M3 && cache->type != type) return DGEN_EINVAL;
     if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads) return DGEN_EINVAL;
     if (static_cast<int64_t>(n_tokens) * n_q_heads > INT32_MAX) return DGEN_EINVAL;
-    if (!std::isfinite(scale) || !(scale > 0.f) || !(cap >= 0.f) || std::isinf(cap) || window < 0 || (causal != 0 && causal != 1))
+    if (!std::isfinite(scale * paged::kLog2e) || !(scale > 0.f) || !(cap >= 0.f) || std::isinf(cap) || window < 0 || (causal != 0 && causal != 1))
         return DGEN_EINVAL;
     if (n_tokens == 0) return DGEN_OK;
     if (!good_rows(q, n_tokens, n_q_heads) || !good_rows_out(out, n_tokens, n_q_heads, cache->head_dim)) return DGEN_EINVAL;

@@ -133,3 +133,11 @@ def test_closed_forms_of_the_unit_walk(tmp_path):
                            os.path.join(os.path.dirname(os.path.abspath(__file__)), "paged_units_check.cu")])
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
+
+
+# ------------------------------------------------------------------ scales
+
+def test_a_scale_beyond_fp32_in_powers_of_two_is_refused():
+    """Scores are kept in powers of two: scale * log2 e is a number of fp32 too."""
+    assert _attend(scale=3e38, ws_bytes=16) == dg.DGEN_EINVAL
+    assert _attend(scale=2.3e38, ws_bytes=16) == dg.DGEN_ESCRATCH
